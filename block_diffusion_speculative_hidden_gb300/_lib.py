@@ -17,14 +17,18 @@ STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "pool
                 7: "too large for the fixed scratch", 8: "not allowed while capturing"}
 ROUND_DEVICE = (1 << 64) - 1   # dflash_accept: take the round from the device counter
 DEV_POOL_EXHAUSTED, DEV_SEQ_TOO_LONG, DEV_WAIT_TIMEOUT, DEV_BAD_TOKEN, DEV_BAD_ROWS, DEV_BAD_BLOCK = 1, 2, 4, 8, 16, 32
+DEV_BAD_PAGE, DEV_BAD_POS = 64, 128
 DTYPE_F32, DTYPE_BF16, DTYPE_BF16_W8 = 0, 1, 2
+ELEM_F32, ELEM_BF16, ELEM_F16 = 0, 1, 2
+W4_INT, W4_E2M1 = 0, 1
 
 EXPORTED = ("dflash_workspace_size", "dflash_kv_pool_size", "dflash_create", "dflash_destroy",
             "dflash_reset", "dflash_release", "dflash_inject_kv", "dflash_draft_block",
             "dflash_accept", "dflash_get_status", "dflash_status_string", "dflash_gemm_bf16",
             "dflash_profile_enable", "dflash_profile_read", "dflash_truncate", "dflash_gemm_bf16_noalloc",
             "dflash_graph_begin", "dflash_graph_end", "dflash_graph_launch", "dflash_graph_destroy",
-            "dflash_gemm_w8", "dflash_block_attention")
+            "dflash_gemm_w8", "dflash_block_attention", "dflash_rope_table", "dflash_extend", "dflash_append_kv",
+            "dflash_prefix_attention", "dflash_prefix_attention_workspace", "dflash_gemm_w4")
 PROF_CLASSES = ("proj", "lm_head", "inject", "attention", "rowwise", "accept")
 
 
@@ -47,6 +51,11 @@ class DflashWeights(ctypes.Structure):
                 ("g_in", _PVP), ("g_post", _PVP),
                 ("s_fc", _VP), ("s_lm", _VP), ("s_kv_inject", _VP),
                 ("s_qkv", _PVP), ("s_o", _PVP), ("s_gu", _PVP), ("s_down", _PVP)]
+
+
+class DflashPagedKV(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in ("k", "v", "page_table", "seq_len")] + [(n, ctypes.c_int) for n in (
+        "n_pages", "n_seqs", "max_pages", "n_kv_heads", "head_dim", "elem")]
 
 
 _lib = None
@@ -109,6 +118,21 @@ def lib() -> ctypes.CDLL:
         L.dflash_graph_launch.argtypes = [_VP, _VP]
         L.dflash_graph_destroy.restype = ctypes.c_int
         L.dflash_graph_destroy.argtypes = [_VP]
+        ci, ll, pkv = ctypes.c_int, ctypes.c_longlong, ctypes.POINTER(DflashPagedKV)
+        L.dflash_rope_table.restype = ci
+        L.dflash_rope_table.argtypes = [_VP, _VP, ci, ci, ctypes.c_double, _VP]
+        L.dflash_extend.restype = ci
+        L.dflash_extend.argtypes = [_VP, i32p, ci, ci, ci, _VP]
+        L.dflash_append_kv.restype = ci
+        L.dflash_append_kv.argtypes = [pkv, _VP, ll, _VP, ll, ci, i32p, i32p, i32p, ci, ci, _VP, _VP, ci, _VP, ll, ci,
+                                       _VP, _VP, _VP]
+        L.dflash_prefix_attention.restype = ci
+        L.dflash_prefix_attention.argtypes = [pkv, _VP, ll, ci, i32p, i32p, ci, ci, i32p, i32p, ci, ci, ctypes.c_float,
+                                              ci, ci, _VP, _VP, _VP, sz, _VP, _VP]
+        L.dflash_prefix_attention_workspace.restype = sz
+        L.dflash_prefix_attention_workspace.argtypes = [pkv, ci, ci, ci, ci, ci, ci]
+        L.dflash_gemm_w4.restype = ci
+        L.dflash_gemm_w4.argtypes = [_VP, ci, _VP, ci, _VP, ci, ci, ci, _VP, ci, ci, _VP, _VP, _VP]
         L.dflash_status_string.restype = ctypes.c_char_p
         L.dflash_status_string.argtypes = [ctypes.c_int]
         _lib = L

@@ -456,7 +456,8 @@ dflash_status dflash_create(const dflash_config* cfg, const dflash_weights* w, v
   // by their values, which must therefore be finite
   if (cudaMemsetAsync(kv_pool, 0, dflash_kv_pool_size(cfg), nullptr) != cudaSuccess ||
       (c->pers_cnt != nullptr && cudaMemsetAsync(c->pers_cnt, 0, sizeof(int) * sms, nullptr) != cudaSuccess) ||
-      launch_rope_table(c, nullptr) != cudaSuccess || launch_reset(c, nullptr) != cudaSuccess ||
+      launch_rope_table(c->rope_cos, c->rope_sin, c->rope_rows, cfg->head_dim, static_cast<double>(cfg->rope_theta),
+                        nullptr) != cudaSuccess || launch_reset(c, nullptr) != cudaSuccess ||
       cudaStreamSynchronize(nullptr) != cudaSuccess) {
     delete c;
     return DFLASH_ERR_CUDA;
@@ -497,6 +498,18 @@ dflash_status dflash_release(dflash_ctx* ctx, int b, dflash_stream stream) {
 dflash_status dflash_truncate(dflash_ctx* ctx, int b, int new_len, dflash_stream stream) {
   if (ctx == nullptr || b < 0 || b >= ctx->cfg.max_batch || new_len < 0) return DFLASH_ERR_INVALID_ARG;
   DF_CHECK(launch_truncate(ctx, b, new_len, stream));
+  return DFLASH_OK;
+}
+
+dflash_status dflash_extend(dflash_ctx* ctx, const int32_t* n_rows, int first_seq, int B, int max_rows,
+                            dflash_stream stream) {
+  if (ctx == nullptr || n_rows == nullptr) return DFLASH_ERR_INVALID_ARG;
+  const dflash_config& g = ctx->cfg;
+  if (B < 1 || first_seq < 0 || first_seq + B > g.max_batch || max_rows < 1) return DFLASH_ERR_INVALID_ARG;
+  if (max_rows > g.max_rows || static_cast<long long>(B) * max_rows > g.max_inject_rows)
+    return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  ProfScope p(ctx, DFLASH_PROF_ROWWISE, 1, stream);
+  DF_CHECK(launch_alloc(ctx, n_rows, first_seq, B, max_rows, stream));
   return DFLASH_OK;
 }
 

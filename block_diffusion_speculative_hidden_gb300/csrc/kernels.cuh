@@ -1,5 +1,5 @@
 // Launch interfaces of the non-GEMM kernels (defined in paging.cu,
-// pointwise.cu, attention.cu and accept.cu).
+// pointwise.cu, attention.cu, accept.cu and prefix_attn.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -14,7 +14,7 @@ cudaError_t launch_reset(dflash_ctx* c, cudaStream_t s);
 cudaError_t launch_release(dflash_ctx* c, int b, cudaStream_t s);
 cudaError_t launch_truncate(dflash_ctx* c, int b, int new_len, cudaStream_t s);
 cudaError_t launch_alloc(dflash_ctx* c, const int32_t* n_rows, int first_seq, int B, int max_rows, cudaStream_t s);
-cudaError_t launch_rope_table(dflash_ctx* c, cudaStream_t s);
+cudaError_t launch_rope_table(float* rope_cos, float* rope_sin, int rows, int head_dim, double theta, cudaStream_t s);
 
 // pointwise.cu (T = the config element type, chosen by c->cfg.dtype)
 cudaError_t launch_gather_rows(dflash_ctx* c, const void* feats, int rows, cudaStream_t s);
@@ -39,6 +39,10 @@ cudaError_t launch_block_attention(dflash_ctx* c, int layer, int NB, const int32
 cudaError_t launch_attention_mma(dflash_ctx* c, int layer, int B, int splits, cudaStream_t s, const NextGemm& next,
                                  const AttnSrc& src = AttnSrc{});
 int attention_mma_splits(dflash_ctx* c, int B);
+
+// prefix_attn.cu
+// Whether a caller's cache description is usable (pointers, counts, alignment; not its head_dim).
+bool paged_kv_ok(const dflash_paged_kv* kv);
 
 // accept.cu
 cudaError_t launch_accept_greedy(int B, int K, const int32_t* d, const int32_t* y, int32_t* tau, int32_t* emitted,

@@ -134,8 +134,8 @@ __global__ void k_alloc(const int32_t* __restrict__ n_rows, int first_seq, int B
 
 // cos/sin of pos * theta^(-2i/dh), computed in double and stored as fp32.
 __global__ void k_rope_table(float* cosb, float* sinb, int rows, int half, int head_dim, double theta) {
-  const int t = blockIdx.x * blockDim.x + threadIdx.x;
-  if (t >= rows * half) return;
+  const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
+  if (t >= static_cast<unsigned>(rows) * half) return;
   const int pos = t / half, i = t % half;
   const double inv = pow(theta, -2.0 * i / head_dim);
   double sn, cs;
@@ -170,11 +170,11 @@ cudaError_t launch_alloc(dflash_ctx* c, const int32_t* n_rows, int first_seq, in
                   c->row_seq, c->row_pos, c->row_src, c->status);
 }
 
-cudaError_t launch_rope_table(dflash_ctx* c, cudaStream_t s) {
-  const int half = c->cfg.head_dim / 2;
-  const int n = c->rope_rows * half;
-  k_rope_table<<<(n + 255) / 256, 256, 0, s>>>(c->rope_cos, c->rope_sin, c->rope_rows, half, c->cfg.head_dim,
-                                               static_cast<double>(c->cfg.rope_theta));
+cudaError_t launch_rope_table(float* rope_cos, float* rope_sin, int rows, int head_dim, double theta,
+                              cudaStream_t s) {
+  const int half = head_dim / 2;
+  const unsigned n = static_cast<unsigned>(rows) * half;
+  k_rope_table<<<(n + 255) / 256, 256, 0, s>>>(rope_cos, rope_sin, rows, half, head_dim, theta);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,708 @@
+// dflash_prefix_attention: attention of a batch over prefixes that groups of
+// sequences share and over each sequence's own tokens, on a paged cache.
+//
+// A query row r sees the keys of its group's prefix and keys of its own
+// sequence.  Softmax attention over a union of key sets splits exactly: with
+// z = scale q.k, each set S gives l_S = log sum_S exp z and o_S = sum_S
+// exp(z - l_S) v, and
+//     out = sum_S exp(l_S - l) o_S,  l = log sum_S exp l_S.
+// So a prefix is read once for all query rows of its group (as one tall
+// matrix of rows), each sequence's own keys for its own rows, either of them
+// in several chunks of pages, and a last kernel joins the partial results in
+// a fixed order.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace dflash {
+
+namespace {
+
+struct PrefixParams {
+  const void* q;
+  long long ld_q;
+  const int32_t *n_rows, *seq, *group_off, *prefix_seq, *page_table, *seq_len;
+  int B, T, Hq, Hkv, G, NG, n_pages, n_seqs, max_pages, causal;
+  float scale_log2;  // scale * log2(e): scores are taken in powers of two
+  void* out;
+  float* lse;
+  float* part_o;    // [chunk][B*T*Hq][DH], normalised by its own sum
+  float* part_lse;  // [chunk][B*T*Hq], in powers of two
+  int* status;
+  int p_tiles, p_chunks;  // prefix parts: row tiles over all groups (a bound), chunks of pages
+  int s_tiles, s_chunks;  // own parts: row tiles of an entry, chunks of pages
+};
+
+// A chunk is no shorter than this, so that a short context is not spread
+// over chunks of a page each.
+constexpr int kMinChunkPages = 8;
+
+__host__ __device__ __forceinline__ int chunk_pages(int pages, int chunks) {
+  const int per = (pages + chunks - 1) / chunks;
+  return per < kMinChunkPages ? kMinChunkPages : per;
+}
+
+__device__ __forceinline__ void flag_status(int* status, int bit) { atomicOr(status, bit); }
+
+// Rows of entry b (0 where n_rows is out of range).
+__device__ __forceinline__ int entry_rows(const PrefixParams& p, int b) {
+  const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
+  return n < 0 || n > p.T ? 0 : n;
+}
+
+// Tokens of the cache's sequence s, at most what its page table can name (0 for a bad index).
+__device__ __forceinline__ int seq_tokens(const PrefixParams& p, int s) {
+  if (s < 0 || s >= p.n_seqs) return 0;
+  return max(0, min(p.seq_len[s], p.max_pages * kPage));
+}
+
+struct Group {
+  int lo, hi;   // its entries
+  int row;      // the prefix's sequence (-1: none)
+  int tokens;   // and length
+  int tile;     // row tile within the group
+};
+
+__device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
+  Group r;
+  r.lo = p.group_off[g];
+  r.hi = p.group_off[g + 1];
+  r.row = p.prefix_seq[g];
+  r.tokens = seq_tokens(p, r.row);
+  r.tile = 0;
+  return r;
+}
+
+// Whether group bounds run from 0 to B without falling (the whole warp asks).
+__device__ __forceinline__ bool bounds_ok(const PrefixParams& p) {
+  const int lane = threadIdx.x & 31;
+  bool ok = p.group_off[0] == 0 && p.group_off[p.NG] == p.B;
+  for (int g = lane; g < p.NG; g += 32) ok = ok && p.group_off[g] <= p.group_off[g + 1];
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The group that row tile `tile` (of `rows` rows) falls in, counting every
+// group's tiles in order (the whole warp asks; false past the last one).
+__device__ __forceinline__ bool find_tile(const PrefixParams& p, int tile, int rows, Group& out) {
+  const int lane = threadIdx.x & 31;
+  for (int g0 = 0; g0 < p.NG; g0 += 32) {
+    const int g = g0 + lane;
+    int n = 0;
+    if (g < p.NG) {
+      const long long r = static_cast<long long>(p.group_off[g + 1] - p.group_off[g]) * p.T * p.G;
+      n = static_cast<int>((r + rows - 1) / rows);
+    }
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, tile < sum);
+    if (past != 0) {
+      const int at = __ffs(past) - 1;
+      const int before = __shfl_sync(0xffffffffu, sum - n, at);
+      out = load_group(p, g0 + at);
+      out.tile = tile - before;
+      return true;
+    }
+    tile -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
+// The group of entry b (the whole warp asks; the bounds are ok).
+__device__ __forceinline__ Group find_entry(const PrefixParams& p, int b) {
+  const int lane = threadIdx.x & 31;
+  for (int g0 = 0; g0 < p.NG; g0 += 32) {
+    const int g = g0 + lane;
+    const unsigned in = __ballot_sync(0xffffffffu, g < p.NG && b >= p.group_off[g] && b < p.group_off[g + 1]);
+    if (in != 0) return load_group(p, g0 + __ffs(in) - 1);
+  }
+  return Group{0, 0, -1, 0, 0};
+}
+
+template <typename T>
+struct Mma16;
+template <>
+struct Mma16<__nv_bfloat16> {
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Mma16<__half> {
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(h), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
+constexpr int kThinWarps = 4;
+constexpr int kThinThreads = kThinWarps * 32;
+constexpr int kThinRows = 16;   // query rows of a tile (one MMA's rows)
+constexpr int kThinStages = 3;  // pages in flight per warp
+
+template <int DH>
+struct ThinLayout {
+  static constexpr int HALF_PAGE = kPage * DH * 2;        // bytes of a page of K (or V) of one head
+  static constexpr int STAGE = 2 * HALF_PAGE;
+  static constexpr int WARP = kThinStages * STAGE;
+  static constexpr int LDO = DH + 8;                      // floats per row of a warp's partial output
+  static constexpr int OFF_ML = kThinWarps * WARP;        // [warps][16][2] maxima and sums
+  static constexpr int OFF_BAR = OFF_ML + kThinWarps * kThinRows * 8;
+  static constexpr int BYTES = OFF_BAR + kThinWarps * kThinStages * 8;
+  static constexpr int SMEM = 1024 + BYTES;
+  static_assert(kThinRows * LDO * 4 <= WARP, "a warp's partial output fits its ring");
+};
+
+// One CTA: a tile of 16 query rows of one kv head over a chunk of pages.
+// Every warp takes every fourth page with a ring of its own, keeps its own
+// running maximum, sum and output, and the CTA joins its warps at the end.
+template <typename T16, int DH>
+__global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
+                                                              const __grid_constant__ CUtensorMap tmV,
+                                                              const __grid_constant__ PrefixParams p) {
+  using L = ThinLayout<DH>;
+  using M = Mma16<T16>;
+  constexpr int KS = DH / 16, NT = DH / 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gr = lane >> 2, t4 = lane & 3;
+
+  // which rows, and which keys
+  const int n_prefix = p.p_tiles * p.Hkv * p.p_chunks;
+  const bool shared = static_cast<int>(blockIdx.x) < n_prefix;
+  int item = shared ? blockIdx.x : blockIdx.x - n_prefix;
+  const int chunks = shared ? p.p_chunks : p.s_chunks;
+  const int chunk = item % chunks;
+  item /= chunks;
+  const int kvh = item % p.Hkv, tile = item / p.Hkv;
+  int b0, row0, rows, tokens, table_row;
+  if (shared) {
+    Group g;
+    if (!bounds_ok(p) || !find_tile(p, tile, kThinRows, g)) return;
+    b0 = g.lo;
+    row0 = g.tile * kThinRows;
+    rows = (g.hi - g.lo) * p.T * p.G;
+    tokens = g.tokens;
+    table_row = g.row;
+    if (chunk == 0 && threadIdx.x == 0 && g.row != -1) {
+      if (g.row < -1 || g.row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
+      else if (p.seq_len[g.row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
+    }
+  } else {
+    const int b = tile / p.s_tiles;
+    b0 = b;
+    row0 = (tile - b * p.s_tiles) * kThinRows;
+    table_row = p.seq != nullptr ? p.seq[b] : b;
+    tokens = seq_tokens(p, table_row);
+    rows = entry_rows(p, b) * p.G;
+    if (chunk == 0 && row0 == 0 && threadIdx.x == 0) {
+      const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
+      if (n < 0 || n > p.T) flag_status(p.status, ST_BAD_ROWS);
+      if (table_row < 0 || table_row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
+      else if (p.seq_len[table_row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
+    }
+  }
+  if (row0 >= rows) return;
+  const int pages = (tokens + kPage - 1) / kPage;
+  const int per = chunk_pages(pages, chunks);
+  const int pg0 = chunk * per, pg1 = min(pages, pg0 + per);
+  // an own part of one chunk without prefixes is the whole result: written even when it holds no key
+  const bool whole = p.NG == 0 && p.s_chunks == 1;
+  if (pg0 >= pg1 && !whole) return;
+
+  // this thread's two rows (gr, gr + 8): their place in q and out, and how many keys they see
+  long long at[2];
+  int seen[2];
+  bool live[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = row0 + gr + 8 * i;
+    live[i] = r < rows;
+    const int tg = p.T * p.G;
+    const int b = live[i] ? b0 + r / tg : b0;
+    const int t = live[i] ? r % tg / p.G : 0, gi = live[i] ? r % p.G : 0;
+    const int n = entry_rows(p, b);
+    live[i] = live[i] && t < n;
+    at[i] = (static_cast<long long>(b) * p.T + t) * p.Hq + kvh * p.G + gi;
+    seen[i] = shared || !p.causal ? tokens : min(tokens, tokens - n + t + 1);
+  }
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * kThinStages;
+  uint8_t* ring = smem + warp * L::WARP;
+  const int mine = pg1 > pg0 + warp ? (pg1 - pg0 - warp + kThinWarps - 1) / kThinWarps : 0;
+  if (lane == 0) {
+    for (int s = 0; s < kThinStages; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  // page ids of this warp's next 32 pages, one per lane
+  int ids = 0;
+  auto fetch_ids = [&](int i0) {
+    const int i = i0 + lane;
+    int id = 0;
+    if (i < mine) {
+      id = p.page_table[static_cast<long long>(table_row) * p.max_pages + pg0 + warp + i * kThinWarps];
+      if (id < 0 || id >= p.n_pages) {
+        flag_status(p.status, ST_BAD_PAGE);
+        id = p.n_pages;  // outside the tensor map: reads as zeros
+      }
+    }
+    ids = id;
+  };
+  auto issue = [&](int i) {
+    if ((i & 31) == 0) fetch_ids(i);
+    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+    if (lane == 0) {
+      const int s = i % kThinStages;
+      const uint32_t kd = smem_u32(ring + s * L::STAGE);
+      mbar_arrive_expect_tx(&bars[s], L::STAGE);
+#pragma unroll
+      for (int c = 0; c < DH / 64; ++c) {
+        tma_page(kd + c * 2048, &tmK, &bars[s], c * 64, kvh, id);
+        tma_page(kd + L::HALF_PAGE + c * 2048, &tmV, &bars[s], c * 64, kvh, id);
+      }
+    }
+  };
+  for (int i = 0; i < min(mine, kThinStages); ++i) issue(i);
+
+  // the query rows as A fragments
+  uint32_t qf[KS][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const long long tok = at[i] / p.Hq;
+    const T16* src = static_cast<const T16*>(p.q) + tok * p.ld_q + (at[i] - tok * p.Hq) * DH + 2 * t4;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      qf[ks][i] = live[i] ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+      qf[ks][2 + i] = live[i] ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+    }
+  }
+
+  float o[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // ldmatrix lane addresses within a [16 keys][128 bytes] swizzled box
+  const int lr = lane & 7, lm = lane >> 3;
+  const int k_key = (lm >> 1) * 8 + lr, k_unit = lm & 1;   // K: matrices (keys, d), (keys, d + 8), (keys + 8, ..)
+  const int v_key = (lm & 1) * 8 + lr, v_unit = lm >> 1;   // V, transposed: (keys, d), (keys + 8, d), (keys, d + 8), ..
+
+  bool ok = true;
+  for (int i = 0; i < mine; ++i) {
+    const int s = i % kThinStages;
+    ok = ok && mbar_wait(&bars[s], (i / kThinStages) & 1, p.status);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const int key0 = (pg0 + warp + i * kThinWarps) * kPage;
+    const uint32_t kd = smem_u32(ring + s * L::STAGE), vd = kd + L::HALF_PAGE;
+    // values past the last token would meet probabilities of zero: they must be finite
+    if (key0 + kPage > tokens) {
+      const int first = tokens - key0;
+      for (int e = lane; e < (kPage - first) * (DH / 64) * 8; e += 32) {
+        const int c = e / ((kPage - first) * 8), f = e % ((kPage - first) * 8);
+        *reinterpret_cast<uint4*>(ring + s * L::STAGE + L::HALF_PAGE + c * 2048 + first * 128 + f * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+    float sc[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t kb[4];
+      const int unit = (ks & 3) * 2 + k_unit;
+      ldsm_x4(kd + (ks >> 2) * 2048 + k_key * 128 + ((unit ^ (k_key & 7)) << 4), kb);
+      M::mma(sc[0], qf[ks], kb[0], kb[1]);
+      M::mma(sc[1], qf[ks], kb[2], kb[3]);
+    }
+    uint32_t pa[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = key0 + (e >> 1) * 8 + 2 * t4 + (e & 1);
+        x[e] = key < seen[h] ? sc[e >> 1][2 * h + (e & 1)] * p.scale_log2 : -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[h], mx), ms = mn == -INFINITY ? 0.f : mn;
+      const float al = exp2f(m[h] - ms);
+      m[h] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = exp2f(x[e] - ms);
+        sum += x[e];
+      }
+      l[h] = l[h] * al + sum;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o[j][2 * h] *= al;
+        o[j][2 * h + 1] *= al;
+      }
+      pa[h] = M::pack(x[0], x[1]);
+      pa[2 + h] = M::pack(x[2], x[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      uint32_t vb[4];
+      const int unit = (j & 7) + v_unit;
+      ldsm_x4_t(vd + (j >> 3) * 2048 + v_key * 128 + ((unit ^ (v_key & 7)) << 4), vb);
+      M::mma(o[j], pa, vb[0], vb[1]);
+      M::mma(o[j + 1], pa, vb[2], vb[3]);
+    }
+    __syncwarp();
+    if (i + kThinStages < mine) issue(i + kThinStages);
+  }
+  if (!ok) {  // a wait gave up: what is still in flight gets its own bounded waits before the CTA leaves
+    for (int s = 0; s < min(mine, kThinStages); ++s) mbar_wait(&bars[s], 0, p.status);
+  }
+
+  // join the warps: each leaves (m, l) and its unnormalised output in its ring
+  float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    const int r = gr + 8 * h;
+    if (t4 == 0) {
+      ml[(warp * kThinRows + r) * 2] = m[h];
+      ml[(warp * kThinRows + r) * 2 + 1] = l[h];
+    }
+    float* dst = reinterpret_cast<float*>(ring) + r * L::LDO + 2 * t4;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+  }
+  __syncthreads();
+  const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
+  const int out_chunk = shared ? chunk : p.p_chunks + chunk;
+  for (int e = threadIdx.x; e < kThinRows * (DH / 4); e += kThinThreads) {
+    const int r = e / (DH / 4), d = (e % (DH / 4)) * 4;
+    const int rr = row0 + r;
+    if (rr >= rows) continue;
+    const int tg = p.T * p.G, b = b0 + rr / tg, t = rr % tg / p.G;
+    if (t >= entry_rows(p, b)) continue;
+    const long long dst = (static_cast<long long>(b) * p.T + t) * p.Hq + kvh * p.G + rr % p.G;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kThinWarps; ++w) mx = fmaxf(mx, ml[(w * kThinRows + r) * 2]);
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThinWarps; ++w) {
+      const float f = exp2f(ml[(w * kThinRows + r) * 2] - ms);
+      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::WARP) + r * L::LDO + d);
+      sum += f * ml[(w * kThinRows + r) * 2 + 1];
+      a.x += f * v.x;
+      a.y += f * v.y;
+      a.z += f * v.z;
+      a.w += f * v.w;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    const float lse2 = sum > 0.f ? ms + log2f(sum) : -INFINITY;
+    if (whole) {
+      *reinterpret_cast<uint2*>(static_cast<T16*>(p.out) + dst * DH + d) = make_uint2(M::pack(a.x, a.y), M::pack(a.z, a.w));
+      if (d == 0 && p.lse != nullptr) p.lse[dst] = lse2 * 0.69314718055994531f;
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (out_chunk * R + dst) * DH + d) = a;
+      if (d == 0) p.part_lse[out_chunk * R + dst] = lse2;
+    }
+  }
+}
+
+constexpr int kJoinWarps = 8;
+
+// out of the partial results: a warp per query row, chunks in order.
+template <typename T16, int DH>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p) {
+  using M = Mma16<T16>;
+  constexpr int E = DH / 32;  // elements a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tok = blockIdx.x, b = tok / p.T, t = tok % p.T;
+  const int h = blockIdx.y * kJoinWarps + warp;
+  if (h >= p.Hq || t >= entry_rows(p, b)) return;
+  const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
+  const long long row = static_cast<long long>(tok) * p.Hq + h;
+  int n_pre = 0;
+  if (p.NG > 0) {
+    if (bounds_ok(p)) {
+      const int pages = (find_entry(p, b).tokens + kPage - 1) / kPage, per = chunk_pages(pages, p.p_chunks);
+      n_pre = (pages + per - 1) / per;
+    } else if (tok == 0 && h == 0 && lane == 0) {
+      flag_status(p.status, ST_BAD_BLOCK);
+    }
+  }
+  const int pages = (seq_tokens(p, p.seq != nullptr ? p.seq[b] : b) + kPage - 1) / kPage;
+  const int per = chunk_pages(pages, p.s_chunks);
+  const int n_all = n_pre + (pages + per - 1) / per;
+  float mx = -INFINITY, sum = 0.f, a[E] = {};
+  auto place = [&](int c) { return static_cast<long long>(c < n_pre ? c : p.p_chunks + c - n_pre) * R + row; };
+  for (int c = lane; c < n_all; c += 32) mx = fmaxf(mx, p.part_lse[place(c)]);
+  mx = warp_max(mx);
+  const float ms = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+  for (int c = 0; c < n_all; ++c) {
+    const long long at = place(c);
+    const float f = exp2f(p.part_lse[at] - ms);
+    const float* src = p.part_o + at * DH + lane * E;
+    if constexpr (E == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      a[0] += f * v.x;
+      a[1] += f * v.y;
+      a[2] += f * v.z;
+      a[3] += f * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      a[0] += f * v.x;
+      a[1] += f * v.y;
+    }
+    sum += f;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  T16* dst = static_cast<T16*>(p.out) + row * DH + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = M::pack(a[e] * inv, a[e + 1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum > 0.f ? (ms + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host side
+
+struct PrefixPlan {
+  long long p_tiles, s_tiles, rows;
+  int p_chunks, s_chunks;
+  size_t off_lse, bytes;
+};
+
+int plan_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 152;
+  }
+  return n;
+}
+
+// Chunks per item: enough for about three CTAs an SM, no chunk of fewer than kMinChunkPages pages.
+int plan_chunks(long long items, int tokens, int sms) {
+  const int pages = (tokens + kPage - 1) / kPage;
+  const long long want = (3ll * sms + items - 1) / items;
+  return static_cast<int>(std::max(1ll, std::min<long long>({want, pages / kMinChunkPages, 128})));
+}
+
+bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_prefix, int max_len, PrefixPlan* out) {
+  const long long tg = static_cast<long long>(T) * (Hq / kv.n_kv_heads);
+  const int cap = kv.max_pages * kPage;
+  const int mp = max_prefix > 0 ? std::min(max_prefix, cap) : cap, ml = max_len > 0 ? std::min(max_len, cap) : cap;
+  PrefixPlan r{};
+  r.rows = static_cast<long long>(B) * T * Hq;
+  r.p_tiles = NG > 0 ? (B * tg + static_cast<long long>(NG) * (kThinRows - 1)) / kThinRows : 0;
+  r.s_tiles = (tg + kThinRows - 1) / kThinRows;
+  const int sms = plan_sms();
+  r.p_chunks = NG > 0 ? plan_chunks(r.p_tiles * kv.n_kv_heads, mp, sms) : 0;
+  r.s_chunks = plan_chunks(B * r.s_tiles * kv.n_kv_heads, ml, sms);
+  if ((r.p_tiles * r.p_chunks + B * r.s_tiles * r.s_chunks) * kv.n_kv_heads > INT32_MAX) return false;
+  const int chunks = NG == 0 && r.s_chunks == 1 ? 0 : r.p_chunks + r.s_chunks;
+  const size_t lse = (sizeof(float) * r.rows * chunks + 255) / 256 * 256;
+  r.off_lse = 256;  // (the first 256 bytes: a status word for callers without one)
+  r.bytes = r.off_lse + lse + sizeof(float) * r.rows * chunks * kv.head_dim;
+  *out = r;
+  return true;
+}
+
+dflash_status check_prefix(const dflash_paged_kv* kv, int Hq, int B, int T, int NG, int max_prefix, int max_len) {
+  if (!paged_kv_ok(kv) || B < 1 || T < 1 || NG < 0 || max_prefix < 0 || max_len < 0 || Hq < 1)
+    return DFLASH_ERR_INVALID_ARG;
+  if (Hq % kv->n_kv_heads) return DFLASH_ERR_INVALID_ARG;
+  if (kv->elem == DFLASH_ELEM_F32 || (kv->head_dim != 64 && kv->head_dim != 128)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  // row counts stay well inside 32 bits, and so do the blocks of the joining kernel
+  if (static_cast<long long>(B) * T * Hq > INT32_MAX / 2 || static_cast<long long>(Hq + 7) / 8 > 65535 ||
+      NG > (1 << 20))
+    return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  return DFLASH_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      ptr = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// Pages of one layer as a 4-D map with boxes of 16 tokens x 64 elements (128-byte swizzled rows).
+bool page_map(const dflash_paged_kv& kv, void* base, CUtensorMap* out) {
+  const auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dh = kv.head_dim;
+  const cuuint64_t gdim[4] = {dh, kPage, static_cast<cuuint64_t>(kv.n_kv_heads), static_cast<cuuint64_t>(kv.n_pages)};
+  const cuuint64_t gstride[3] = {dh * 2, dh * 2 * kPage, dh * 2 * kPage * kv.n_kv_heads};
+  const cuuint32_t box[4] = {64, kPage, 1, 1}, es[4] = {1, 1, 1, 1};
+  return fn(out, kv.elem == DFLASH_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            base, gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T16, int DH>
+cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  static FuncAttr attr;
+  cudaError_t e = attr.ensure(ThinLayout<DH>::SMEM, [](int v) {
+    return cudaFuncSetAttribute(k_prefix_thin<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+  });
+  if (e != cudaSuccess) return e;
+  const long long blocks =
+      (static_cast<long long>(p.p_tiles) * p.p_chunks + static_cast<long long>(p.B) * p.s_tiles * p.s_chunks) * p.Hkv;
+  e = launch_k(k_prefix_thin<T16, DH>, dim3(static_cast<unsigned>(blocks)), dim3(kThinThreads), ThinLayout<DH>::SMEM,
+               s, dim3(1), false, tk, tv, p);
+  if (e != cudaSuccess || (p.NG == 0 && p.s_chunks == 1)) return e;
+  return launch_k(k_prefix_join<T16, DH>, dim3(p.B * p.T, (p.Hq + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32),
+                  0, s, dim3(1), false, p);
+}
+
+}  // namespace
+
+bool paged_kv_ok(const dflash_paged_kv* kv) {
+  if (kv == nullptr || kv->k == nullptr || kv->v == nullptr || kv->page_table == nullptr || kv->seq_len == nullptr)
+    return false;
+  if (kv->n_pages < 1 || kv->n_seqs < 1 || kv->max_pages < 1 || kv->max_pages > INT32_MAX / (2 * kPage) ||
+      kv->n_kv_heads < 1 || kv->head_dim < 1)
+    return false;
+  if (kv->elem != DFLASH_ELEM_F32 && kv->elem != DFLASH_ELEM_BF16 && kv->elem != DFLASH_ELEM_F16) return false;
+  return reinterpret_cast<uintptr_t>(kv->k) % 16 == 0 && reinterpret_cast<uintptr_t>(kv->v) % 16 == 0;
+}
+
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" {
+
+size_t dflash_prefix_attention_workspace(const dflash_paged_kv* kv, int n_q_heads, int B, int T, int NG,
+                                         int max_prefix, int max_len) {
+  PrefixPlan plan;
+  if (check_prefix(kv, n_q_heads, B, T, NG, max_prefix, max_len) != DFLASH_OK ||
+      !make_plan(*kv, n_q_heads, B, T, NG, max_prefix, max_len, &plan))
+    return 0;
+  return plan.bytes;
+}
+
+dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, long long ld_q, int n_q_heads,
+                                      const int32_t* n_rows, const int32_t* seq, int B, int T,
+                                      const int32_t* group_off, const int32_t* prefix_seq, int NG, int causal,
+                                      float scale, int max_prefix, int max_len, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, int* status, dflash_stream stream) {
+  const dflash_status st = check_prefix(kv, n_q_heads, B, T, NG, max_prefix, max_len);
+  if (st != DFLASH_OK) return st;
+  if (q == nullptr || out == nullptr || workspace == nullptr || !(scale >= 0.f) || scale > 3e38f)
+    return DFLASH_ERR_INVALID_ARG;
+  if (NG > 0 ? group_off == nullptr || prefix_seq == nullptr : group_off != nullptr || prefix_seq != nullptr)
+    return DFLASH_ERR_INVALID_ARG;
+  if (seq == nullptr && B > kv->n_seqs) return DFLASH_ERR_INVALID_ARG;
+  const auto addr = [](const void* a) { return reinterpret_cast<uintptr_t>(a); };
+  const long long qd = static_cast<long long>(n_q_heads) * kv->head_dim;
+  const bool one = static_cast<long long>(B) * T == 1;
+  if (addr(q) % 16 || addr(out) % 16 || addr(workspace) % 256 || (!one && (ld_q % 8 || ld_q < qd)) ||
+      (q == out && !one && ld_q != qd))
+    return DFLASH_ERR_INVALID_ARG;
+  PrefixPlan plan;
+  if (!make_plan(*kv, n_q_heads, B, T, NG, max_prefix, max_len, &plan)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < plan.bytes) return DFLASH_ERR_WORKSPACE;
+  CUtensorMap tk, tv;
+  if (!page_map(*kv, kv->k, &tk) || !page_map(*kv, kv->v, &tv)) return DFLASH_ERR_CUDA;
+  PrefixParams p{};
+  p.q = q;
+  p.ld_q = one ? 0 : ld_q;
+  p.n_rows = n_rows;
+  p.seq = seq;
+  p.group_off = group_off;
+  p.prefix_seq = prefix_seq;
+  p.page_table = kv->page_table;
+  p.seq_len = kv->seq_len;
+  p.B = B;
+  p.T = T;
+  p.Hq = n_q_heads;
+  p.Hkv = kv->n_kv_heads;
+  p.G = n_q_heads / kv->n_kv_heads;
+  p.NG = NG;
+  p.n_pages = kv->n_pages;
+  p.n_seqs = kv->n_seqs;
+  p.max_pages = kv->max_pages;
+  p.causal = causal;
+  p.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(kv->head_dim))) * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  const int chunks = plan.p_chunks + plan.s_chunks;
+  p.part_lse = reinterpret_cast<float*>(ws + plan.off_lse);
+  p.part_o = reinterpret_cast<float*>(ws + plan.off_lse + (sizeof(float) * plan.rows * chunks + 255) / 256 * 256);
+  p.status = status != nullptr ? status : reinterpret_cast<int*>(ws);
+  p.p_tiles = static_cast<int>(plan.p_tiles);
+  p.p_chunks = plan.p_chunks;
+  p.s_tiles = static_cast<int>(plan.s_tiles);
+  p.s_chunks = plan.s_chunks;
+  cudaError_t e;
+  if (kv->elem == DFLASH_ELEM_BF16)
+    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, tk, tv, stream)
+                           : launch_prefix<__nv_bfloat16, 128>(p, tk, tv, stream);
+  else
+    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, tk, tv, stream)
+                           : launch_prefix<__half, 128>(p, tk, tv, stream);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -14,6 +14,7 @@ from typing import Dict, Optional
 import torch
 
 from . import _lib
+from .decode import PagedKV
 
 _DTYPES = {"bf16": (_lib.DTYPE_BF16, torch.bfloat16), "f32": (_lib.DTYPE_F32, torch.float32)}
 
@@ -249,6 +250,12 @@ class Drafter:
         shp = (s.n_layers, pages, s.n_kv_heads, 16, s.head_dim)
         return flat[:n].view(shp), flat[n:2 * n].view(shp)
 
+    def paged_kv(self, layer: int) -> PagedKV:
+        """The context cache of one draft layer, for append_kv and prefix_attention."""
+        k, v = self.pool_kv()
+        n = self.cfg.n_pages
+        return PagedKV(k[layer, :n], v[layer, :n], self.page_table, self.seq_len)
+
     # ------------------------------------------------------------------ the ABI calls
     def inject_kv(self, feats: torch.Tensor, n_rows: torch.Tensor, first_seq: int = 0, stream=None) -> None:
         """feats [B, max_rows, n_taps*tap_width] (config dtype), n_rows int32 [B] on the device."""
@@ -256,6 +263,15 @@ class Drafter:
         assert feats.is_contiguous() and feats.dtype == self.tdtype and n_rows.dtype == torch.int32
         _lib.check(self.L.dflash_inject_kv(self.ctx, _ptr(feats), _ptr(n_rows), first_seq, B, max_rows,
                                            _stream(stream)), "dflash_inject_kv")
+
+    def extend(self, n_rows: torch.Tensor, first_seq: int = 0, max_rows: Optional[int] = None, stream=None) -> None:
+        """Room for n_rows[i] (int32 on the device, at most max_rows) more tokens in
+        sequences first_seq + i; append_kv then fills it, once per layer."""
+        if n_rows.dtype != torch.int32 or not n_rows.is_contiguous() or n_rows.device != self.seq_len.device:
+            raise ValueError("n_rows: contiguous int32 on the context's device")
+        _lib.check(self.L.dflash_extend(self.ctx, _ptr(n_rows), first_seq, n_rows.numel(),
+                                        self.cfg.max_rows if max_rows is None else max_rows, _stream(stream)),
+                   "dflash_extend")
 
     def draft_block(self, B: int, S: int = 1, tokens: Optional[torch.Tensor] = None,
                     conf: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,

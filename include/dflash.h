@@ -69,7 +69,10 @@ typedef enum {
 #define DFLASH_DEV_WAIT_TIMEOUT 4   /* a bounded device wait gave up (2 s) */
 #define DFLASH_DEV_BAD_TOKEN 8      /* a token id outside [0, vocab) */
 #define DFLASH_DEV_BAD_ROWS 16      /* an n_rows entry outside [0, max_rows] */
-#define DFLASH_DEV_BAD_BLOCK 32     /* dflash_block_attention: a block's sequence or prefix out of range */
+#define DFLASH_DEV_BAD_BLOCK 32     /* a sequence index or prefix out of range (dflash_block_attention, dflash_append_kv,
+                                       dflash_prefix_attention) */
+#define DFLASH_DEV_BAD_PAGE 64      /* a page-table entry outside [0, n_pages) where a sequence holds tokens */
+#define DFLASH_DEV_BAD_POS 128      /* a position outside the rotation table */
 
 /* DFLASH_BF16_W8: DFLASH_BF16 with FP8 projection weights.  Every projection
  * weight (w_fc, w_kv_inject, w_qkv, w_o, w_gu, w_down, w_lm) is one E4M3 code
@@ -371,6 +374,161 @@ dflash_status dflash_gemm_w8(const void* W, const float* w_scale, int N, int K, 
 dflash_status dflash_gemm_bf16_noalloc(const void* W, int N, int K, const void* X, const void* X_lo, int M,
                                        float* out, int splits, int* splits_used, int* status,
                                        dflash_stream stream);
+
+/* ---- The caller's own decode and verification steps -----------------------
+ *
+ * The next four calls serve the layers around the drafter: the target (or
+ * any other model) that decodes token by token or verifies the K + 1
+ * positions of a drafted block on a paged cache of the same form as the
+ * draft cache.  They need no context and no projection weights: the caller
+ * names its tensors, and a cache in the caller's memory.  A context's own
+ * pool has this form too (dflash_kv_pool_size; pages n_pages .. of a layer
+ * are its block pages and belong to dflash_draft_block). */
+
+/* Element types of the calls below. */
+typedef enum { DFLASH_ELEM_F32 = 0, DFLASH_ELEM_BF16 = 1, DFLASH_ELEM_F16 = 2 } dflash_elem;
+
+/* One layer of a paged KV cache.  Token j of sequence s lies in page
+ * page_table[s][j / 16] at slot j % 16.  Entries of the page table past a
+ * sequence's length are not read. */
+typedef struct {
+  void* k;                   /* device [n_pages][n_kv_heads][16][head_dim], 16-byte aligned */
+  void* v;                   /* as k */
+  const int32_t* page_table; /* device [n_seqs][max_pages] */
+  const int32_t* seq_len;    /* device [n_seqs]: tokens of every sequence */
+  int n_pages, n_seqs, max_pages, n_kv_heads;
+  int head_dim;              /* 32, 64 or 128 */
+  int elem;                  /* dflash_elem of k and v */
+} dflash_paged_kv;
+
+/* cos and sin (device fp32 [rows][head_dim / 2], written) of
+ * pos * theta^(-2i / head_dim), computed in double. */
+dflash_status dflash_rope_table(float* rope_cos, float* rope_sin, int rows, int head_dim, double theta,
+                                dflash_stream stream);
+
+/* Give the context's sequences first_seq .. first_seq + B - 1 room for
+ * n_rows[b - first_seq] more tokens (device int32, each in [0, max_rows]):
+ * the page allocation of dflash_inject_kv without its projections, under
+ * the same rules and limits.  The new slots hold what the pages held before
+ * until dflash_append_kv (once per layer) fills them.  Asynchronous. */
+dflash_status dflash_extend(dflash_ctx* ctx, const int32_t* n_rows, int first_seq, int B, int max_rows,
+                            dflash_stream stream);
+
+/* Append keys and values to a paged cache, rotating the keys (and the
+ * step's queries) on the way.
+ *
+ * For batch entry b = 0 .. B-1 of sequence s = seq[b] (device int32 [B];
+ * NULL: s = b) the n = n_rows[b] (device int32 [B], each in [0, T]; NULL: T)
+ * rows k[b][i], v[b][i], i < n, become the last n tokens of the sequence:
+ * slots seq_len[s] - n + i.  seq_len already counts them, so the call can be
+ * made once per layer under one set of lengths.  Row i stands at position
+ * pos_base[b] + slot (device int32 [B]; NULL: 0), which pos_base sets to the
+ * length of a prefix kept in another sequence.  With a rotation table
+ * (rope_cos, rope_sin device fp32 [rope_rows][head_dim / 2], 16-byte
+ * aligned; both NULL: no rotation) key elements (x_i, x_{i + head_dim/2})
+ * become (x_i c - x_{i+h} s, x_{i+h} c + x_i s) in fp32, rounded once to the
+ * cache's type; values are only rounded.  With q (NULL: none), q_out[b][i]
+ * (device [B][T][n_q_heads][head_dim], the cache's type, 16-byte aligned) is q[b][i]
+ * rotated alike.
+ *
+ * q, k, v: device, type src_elem, [B][T][heads][head_dim] with token (b, i)
+ * at element (b * T + i) * ld_{q,k,v} and its heads contiguous from there, so
+ * they may be slices of one projection's output rows.  q_out must not
+ * overlap the inputs.  Entries of seq must differ from each other (two
+ * entries of one sequence write the same slots), and so must the pages that
+ * their new tokens lie in.
+ * On the device an entry with n outside [0, T] (BAD_ROWS), s outside
+ * [0, n_seqs) (BAD_BLOCK), n > seq_len[s] (BAD_ROWS) or
+ * seq_len[s] > 16 * max_pages (SEQ_TOO_LONG) is skipped, and so is a single
+ * row on a bad page (BAD_PAGE) or at a position outside the table (BAD_POS);
+ * the bit is OR-ed into *status (device int32; NULL: not reported).  Rows
+ * i >= n of q_out are left as they were.  Asynchronous, allocates nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (head_dim, or more than 2^31 - 1
+ * tokens or thread blocks), CUDA. */
+dflash_status dflash_append_kv(const dflash_paged_kv* kv, const void* k, long long ld_k, const void* v, long long ld_v,
+                               int src_elem, const int32_t* n_rows, const int32_t* seq, const int32_t* pos_base,
+                               int B, int T, const float* rope_cos, const float* rope_sin, int rope_rows,
+                               const void* q, long long ld_q, int n_q_heads, void* q_out, int* status,
+                               dflash_stream stream);
+
+/* Attention of a batch whose sequences share prefixes.
+ *
+ * Batch entry b attends with its n = n_rows[b] query rows (device int32 [B],
+ * each in [0, T]; NULL: T) to the tokens of a prefix that its group shares
+ * and to its own sequence s = seq[b] (device int32 [B]; NULL: s = b).
+ * Groups are runs of batch entries: group g = 0 .. NG-1 holds entries
+ * group_off[g] .. group_off[g + 1] - 1 (device int32 [NG + 1],
+ * non-decreasing from 0 to B) and its prefix is the whole of the cache's
+ * sequence prefix_seq[g] (device int32 [NG]; -1: none).  NG = 0 (both NULL):
+ * no prefixes.  A prefix is stored once and read once for all query rows of
+ * its group.
+ *
+ * Every row sees the whole prefix.  Of its own sequence of length L row i
+ * sees tokens j <= L - n + i when causal is non-zero (the n rows are its last
+ * n tokens) and all L otherwise.  out[b][i][h] = softmax(scale q k^T) v over
+ * the tokens it sees, query head h reading kv head h / (n_q_heads /
+ * n_kv_heads); scale 0 means 1 / sqrt(head_dim).  A row that sees nothing
+ * gives 0, and its log-sum-exp is -infinity.  lse (device fp32
+ * [B][T][n_q_heads]; NULL: none) gets log sum exp(scale q k^T).  Rows i >= n
+ * of out and lse are left as they were.
+ *
+ * q: device, the cache's type (DFLASH_ELEM_BF16 or DFLASH_ELEM_F16; an fp32
+ * cache returns UNSUPPORTED_SHAPE), token (b, i) at element (b * T + i) * ld_q,
+ * heads contiguous; q 16-byte aligned and ld_q a multiple of 8.  out: device
+ * [B][T][n_q_heads][head_dim], the same type, 16-byte aligned; it may be q
+ * itself only if ld_q = n_q_heads * head_dim and it is the same address.
+ * head_dim 64 or 128; n_q_heads a multiple of n_kv_heads.  Scores, running
+ * maxima and sums and the output accumulate in fp32; probabilities enter the
+ * second product in the cache's type.  What the cache holds past a length
+ * has no effect (NaN included); a non-finite value within the tokens that
+ * some row of an entry sees may reach all rows of that entry.
+ *
+ * max_prefix, max_len: upper bounds of the prefix and sequence lengths that
+ * size the launch (0: 16 * max_pages); longer ones are attended in full all
+ * the same.  workspace: device, 256-byte aligned, at least
+ * dflash_prefix_attention_workspace of the same arguments; it carries nothing
+ * from call to call, and calls that may run at the same time need one each.
+ * On the device an entry with n outside [0, T] (BAD_ROWS), a sequence or
+ * prefix index or group bounds out of range (BAD_BLOCK), a length past
+ * 16 * max_pages (SEQ_TOO_LONG) or a bad page (BAD_PAGE) sets its bit in
+ * *status (device int32; NULL: not reported) and is read as n = 0, as length
+ * 0, as its first 16 * max_pages tokens and as a page of zeros.
+ * Asynchronous, allocates nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * WORKSPACE, CUDA. */
+dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, long long ld_q, int n_q_heads,
+                                      const int32_t* n_rows, const int32_t* seq, int B, int T,
+                                      const int32_t* group_off, const int32_t* prefix_seq, int NG, int causal,
+                                      float scale, int max_prefix, int max_len, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, int* status, dflash_stream stream);
+
+/* Bytes of workspace of dflash_prefix_attention; 0 for arguments that it refuses. */
+size_t dflash_prefix_attention_workspace(const dflash_paged_kv* kv, int n_q_heads, int B, int T, int NG,
+                                         int max_prefix, int max_len);
+
+/* Code formats of dflash_gemm_w4. */
+typedef enum { DFLASH_W4_INT = 0, DFLASH_W4_E2M1 = 1 } dflash_w4_format;
+
+/* Matrix-vector products with 4-bit weights and group scales, for a few rows
+ * of activations: out[m][n] = sum_k X[m][k] * scale[n][k / group] * w[n][k],
+ * beside dflash_gemm_bf16 and dflash_gemm_w8.
+ *
+ * W: device uint8 [N][K / 2], byte j of a row holding the code of element 2j
+ * in its low and of 2j + 1 in its high half.  DFLASH_W4_INT: w = code -
+ * zero[n][k / group], with zero device uint8 [N][ceil(K / group)], each at
+ * most 128 (larger ones are read as 128), or NULL for 8.  DFLASH_W4_E2M1: a
+ * sign, two exponent bits of bias 1 and a mantissa bit (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives); zero must be NULL.  scale: device
+ * [N][ceil(K / group)] of type scale_elem; group 32, 64 or 128 (the last one
+ * of a row may be short).  X: device [M][K], x_elem DFLASH_ELEM_BF16 or
+ * DFLASH_ELEM_F16, 1 <= M <= 32; K a multiple of 32; W and X 16-byte aligned.
+ * out: device fp32 [M][N].  Weights enter the product as the exact code
+ * differences and scales apply to fp32 sums of a group, so nothing is rounded
+ * below fp32.  status: device int32 (NULL: not reported), where a bounded
+ * wait that gives up sets DFLASH_DEV_WAIT_TIMEOUT.  Asynchronous, allocates
+ * nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE (M > 32, K, group), CUDA. */
+dflash_status dflash_gemm_w4(const void* W, int format, const void* scale, int scale_elem, const void* zero, int N,
+                             int K, int group, const void* X, int x_elem, int M, float* out, int* status,
+                             dflash_stream stream);
 
 /* Kernel timing classes of dflash_profile_read. */
 #define DFLASH_PROF_PROJ 0      /* draft-layer projections (QKV, O, gate/up, down) */
