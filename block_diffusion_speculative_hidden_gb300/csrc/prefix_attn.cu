@@ -14,147 +14,11 @@
 
 #include <algorithm>
 
-#include "common.cuh"
-#include "kernels.cuh"
+#include "prefix_common.cuh"
 
 namespace dflash {
 
 namespace {
-
-struct PrefixParams {
-  const void* q;
-  long long ld_q;
-  const int32_t *n_rows, *seq, *group_off, *prefix_seq, *page_table, *seq_len;
-  int B, T, Hq, Hkv, G, NG, n_pages, n_seqs, max_pages, causal;
-  float scale_log2;  // scale * log2(e): scores are taken in powers of two
-  void* out;
-  float* lse;
-  float* part_o;    // [chunk][B*T*Hq][DH], normalised by its own sum
-  float* part_lse;  // [chunk][B*T*Hq], in powers of two
-  int* status;
-  int p_tiles, p_chunks;  // prefix parts: row tiles over all groups (a bound), chunks of pages
-  int s_tiles, s_chunks;  // own parts: row tiles of an entry, chunks of pages
-};
-
-// A chunk is no shorter than this, so that a short context is not spread
-// over chunks of a page each.
-constexpr int kMinChunkPages = 8;
-
-__host__ __device__ __forceinline__ int chunk_pages(int pages, int chunks) {
-  const int per = (pages + chunks - 1) / chunks;
-  return per < kMinChunkPages ? kMinChunkPages : per;
-}
-
-__device__ __forceinline__ void flag_status(int* status, int bit) { atomicOr(status, bit); }
-
-// Rows of entry b (0 where n_rows is out of range).
-__device__ __forceinline__ int entry_rows(const PrefixParams& p, int b) {
-  const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
-  return n < 0 || n > p.T ? 0 : n;
-}
-
-// Tokens of the cache's sequence s, at most what its page table can name (0 for a bad index).
-__device__ __forceinline__ int seq_tokens(const PrefixParams& p, int s) {
-  if (s < 0 || s >= p.n_seqs) return 0;
-  return max(0, min(p.seq_len[s], p.max_pages * kPage));
-}
-
-struct Group {
-  int lo, hi;   // its entries
-  int row;      // the prefix's sequence (-1: none)
-  int tokens;   // and length
-  int tile;     // row tile within the group
-};
-
-__device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
-  Group r;
-  r.lo = p.group_off[g];
-  r.hi = p.group_off[g + 1];
-  r.row = p.prefix_seq[g];
-  r.tokens = seq_tokens(p, r.row);
-  r.tile = 0;
-  return r;
-}
-
-// Whether group bounds run from 0 to B without falling (the whole warp asks).
-__device__ __forceinline__ bool bounds_ok(const PrefixParams& p) {
-  const int lane = threadIdx.x & 31;
-  bool ok = p.group_off[0] == 0 && p.group_off[p.NG] == p.B;
-  for (int g = lane; g < p.NG; g += 32) ok = ok && p.group_off[g] <= p.group_off[g + 1];
-  return __all_sync(0xffffffffu, ok);
-}
-
-// The group that row tile `tile` (of `rows` rows) falls in, counting every
-// group's tiles in order (the whole warp asks; false past the last one).
-__device__ __forceinline__ bool find_tile(const PrefixParams& p, int tile, int rows, Group& out) {
-  const int lane = threadIdx.x & 31;
-  for (int g0 = 0; g0 < p.NG; g0 += 32) {
-    const int g = g0 + lane;
-    int n = 0;
-    if (g < p.NG) {
-      const long long r = static_cast<long long>(p.group_off[g + 1] - p.group_off[g]) * p.T * p.G;
-      n = static_cast<int>((r + rows - 1) / rows);
-    }
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, tile < sum);
-    if (past != 0) {
-      const int at = __ffs(past) - 1;
-      const int before = __shfl_sync(0xffffffffu, sum - n, at);
-      out = load_group(p, g0 + at);
-      out.tile = tile - before;
-      return true;
-    }
-    tile -= __shfl_sync(0xffffffffu, sum, 31);
-  }
-  return false;
-}
-
-// The group of entry b (the whole warp asks; the bounds are ok).
-__device__ __forceinline__ Group find_entry(const PrefixParams& p, int b) {
-  const int lane = threadIdx.x & 31;
-  for (int g0 = 0; g0 < p.NG; g0 += 32) {
-    const int g = g0 + lane;
-    const unsigned in = __ballot_sync(0xffffffffu, g < p.NG && b >= p.group_off[g] && b < p.group_off[g + 1]);
-    if (in != 0) return load_group(p, g0 + __ffs(in) - 1);
-  }
-  return Group{0, 0, -1, 0, 0};
-}
-
-template <typename T>
-struct Mma16;
-template <>
-struct Mma16<__nv_bfloat16> {
-  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
-template <>
-struct Mma16<__half> {
-  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-};
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -167,14 +31,6 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(h), "r"(page), "r"(smem_u32(bar))
-      : "memory");
 }
 
 constexpr int kThinWarps = 4;
@@ -201,7 +57,7 @@ struct ThinLayout {
 template <typename T16, int DH>
 __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
-                                                              const __grid_constant__ PrefixParams p) {
+                                                              const __grid_constant__ PrefixParams p, int n_prefix) {
   using L = ThinLayout<DH>;
   using M = Mma16<T16>;
   constexpr int KS = DH / 16, NT = DH / 8;
@@ -210,65 +66,12 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gr = lane >> 2, t4 = lane & 3;
 
-  // which rows, and which keys
-  const int n_prefix = p.p_tiles * p.Hkv * p.p_chunks;
-  const bool shared = static_cast<int>(blockIdx.x) < n_prefix;
-  int item = shared ? blockIdx.x : blockIdx.x - n_prefix;
-  const int chunks = shared ? p.p_chunks : p.s_chunks;
-  const int chunk = item % chunks;
-  item /= chunks;
-  const int kvh = item % p.Hkv, tile = item / p.Hkv;
-  int b0, row0, rows, tokens, table_row;
-  if (shared) {
-    Group g;
-    if (!bounds_ok(p) || !find_tile(p, tile, kThinRows, g)) return;
-    b0 = g.lo;
-    row0 = g.tile * kThinRows;
-    rows = (g.hi - g.lo) * p.T * p.G;
-    tokens = g.tokens;
-    table_row = g.row;
-    if (chunk == 0 && threadIdx.x == 0 && g.row != -1) {
-      if (g.row < -1 || g.row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
-      else if (p.seq_len[g.row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
-    }
-  } else {
-    const int b = tile / p.s_tiles;
-    b0 = b;
-    row0 = (tile - b * p.s_tiles) * kThinRows;
-    table_row = p.seq != nullptr ? p.seq[b] : b;
-    tokens = seq_tokens(p, table_row);
-    rows = entry_rows(p, b) * p.G;
-    if (chunk == 0 && row0 == 0 && threadIdx.x == 0) {
-      const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
-      if (n < 0 || n > p.T) flag_status(p.status, ST_BAD_ROWS);
-      if (table_row < 0 || table_row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
-      else if (p.seq_len[table_row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
-    }
-  }
-  if (row0 >= rows) return;
-  const int pages = (tokens + kPage - 1) / kPage;
-  const int per = chunk_pages(pages, chunks);
-  const int pg0 = chunk * per, pg1 = min(pages, pg0 + per);
-  // an own part of one chunk without prefixes is the whole result: written even when it holds no key
-  const bool whole = p.NG == 0 && p.s_chunks == 1;
-  if (pg0 >= pg1 && !whole) return;
-
-  // this thread's two rows (gr, gr + 8): their place in q and out, and how many keys they see
-  long long at[2];
-  int seen[2];
-  bool live[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = row0 + gr + 8 * i;
-    live[i] = r < rows;
-    const int tg = p.T * p.G;
-    const int b = live[i] ? b0 + r / tg : b0;
-    const int t = live[i] ? r % tg / p.G : 0, gi = live[i] ? r % p.G : 0;
-    const int n = entry_rows(p, b);
-    live[i] = live[i] && t < n;
-    at[i] = (static_cast<long long>(b) * p.T + t) * p.Hq + kvh * p.G + gi;
-    seen[i] = shared || !p.causal ? tokens : min(tokens, tokens - n + t + 1);
-  }
+  Item it;
+  // (the kernel before it, where there is one, is waited for on every way
+  // out: the joining kernel behind starts once all of this one has left)
+  if (!find_item(p, blockIdx.x, n_prefix, kThinRows, it)) return pdl_wait();
+  const int pg0 = it.pg0, pg1 = it.pg1, tokens = it.tokens, kvh = it.kvh;
+  const Row row[2] = {find_row(p, it, it.row0 + gr), find_row(p, it, it.row0 + gr + 8)};
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * kThinStages;
   uint8_t* ring = smem + warp * L::WARP;
@@ -285,7 +88,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     const int i = i0 + lane;
     int id = 0;
     if (i < mine) {
-      id = p.page_table[static_cast<long long>(table_row) * p.max_pages + pg0 + warp + i * kThinWarps];
+      id = p.page_table[static_cast<long long>(it.table_row) * p.max_pages + pg0 + warp + i * kThinWarps];
       if (id < 0 || id >= p.n_pages) {
         flag_status(p.status, ST_BAD_PAGE);
         id = p.n_pages;  // outside the tensor map: reads as zeros
@@ -313,12 +116,11 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
   uint32_t qf[KS][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const long long tok = at[i] / p.Hq;
-    const T16* src = static_cast<const T16*>(p.q) + tok * p.ld_q + (at[i] - tok * p.Hq) * DH + 2 * t4;
+    const T16* src = static_cast<const T16*>(p.q) + row[i].token * p.ld_q + (row[i].at - row[i].token * p.Hq) * DH + 2 * t4;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      qf[ks][i] = live[i] ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
-      qf[ks][2 + i] = live[i] ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+      qf[ks][i] = row[i].live ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+      qf[ks][2 + i] = row[i].live ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
     }
   }
 
@@ -366,7 +168,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int key = key0 + (e >> 1) * 8 + 2 * t4 + (e & 1);
-        x[e] = key < seen[h] ? sc[e >> 1][2 * h + (e & 1)] * p.scale_log2 : -INFINITY;
+        x[e] = key < row[h].seen ? sc[e >> 1][2 * h + (e & 1)] * p.scale_log2 : -INFINITY;
       }
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -421,25 +223,22 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
   }
   __syncthreads();
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-  const int out_chunk = shared ? chunk : p.p_chunks + chunk;
+  const int out_chunk = it.shared ? it.chunk : p.p_chunks + it.chunk;
   for (int e = threadIdx.x; e < kThinRows * (DH / 4); e += kThinThreads) {
     const int r = e / (DH / 4), d = (e % (DH / 4)) * 4;
-    const int rr = row0 + r;
-    if (rr >= rows) continue;
-    const int tg = p.T * p.G, b = b0 + rr / tg, t = rr % tg / p.G;
-    if (t >= entry_rows(p, b)) continue;
-    const long long dst = (static_cast<long long>(b) * p.T + t) * p.Hq + kvh * p.G + rr % p.G;
+    const Row w = find_row(p, it, it.row0 + r);
+    if (!w.live) continue;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kThinWarps; ++w) mx = fmaxf(mx, ml[(w * kThinRows + r) * 2]);
+    for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
     const float ms = mx == -INFINITY ? 0.f : mx;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThinWarps; ++w) {
-      const float f = exp2f(ml[(w * kThinRows + r) * 2] - ms);
-      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::WARP) + r * L::LDO + d);
-      sum += f * ml[(w * kThinRows + r) * 2 + 1];
+    for (int q = 0; q < kThinWarps; ++q) {
+      const float f = exp2f(ml[(q * kThinRows + r) * 2] - ms);
+      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + q * L::WARP) + r * L::LDO + d);
+      sum += f * ml[(q * kThinRows + r) * 2 + 1];
       a.x += f * v.x;
       a.y += f * v.y;
       a.z += f * v.z;
@@ -448,14 +247,15 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     const float lse2 = sum > 0.f ? ms + log2f(sum) : -INFINITY;
-    if (whole) {
-      *reinterpret_cast<uint2*>(static_cast<T16*>(p.out) + dst * DH + d) = make_uint2(M::pack(a.x, a.y), M::pack(a.z, a.w));
-      if (d == 0 && p.lse != nullptr) p.lse[dst] = lse2 * 0.69314718055994531f;
+    if (it.whole) {
+      *reinterpret_cast<uint2*>(static_cast<T16*>(p.out) + w.at * DH + d) = make_uint2(M::pack(a.x, a.y), M::pack(a.z, a.w));
+      if (d == 0 && p.lse != nullptr) p.lse[w.at] = lse2 * 0.69314718055994531f;
     } else {
-      *reinterpret_cast<float4*>(p.part_o + (out_chunk * R + dst) * DH + d) = a;
-      if (d == 0) p.part_lse[out_chunk * R + dst] = lse2;
+      *reinterpret_cast<float4*>(p.part_o + (out_chunk * R + w.at) * DH + d) = a;
+      if (d == 0) p.part_lse[out_chunk * R + w.at] = lse2;
     }
   }
+  pdl_wait();
 }
 
 constexpr int kJoinWarps = 8;
@@ -468,6 +268,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = blockIdx.x, b = tok / p.T, t = tok % p.T;
   const int h = blockIdx.y * kJoinWarps + warp;
+  pdl_wait();
   if (h >= p.Hq || t >= entry_rows(p, b)) return;
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
   const long long row = static_cast<long long>(tok) * p.Hq + h;
@@ -515,8 +316,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 
 // ------------------------------------------------------------------ host side
 
+// From this many query rows (of an entry; of a group on average) on, the
+// wide kernel takes them.
+constexpr int kWideFrom = 48;
+
 struct PrefixPlan {
-  long long p_tiles, s_tiles, rows;
+  bool p_wide, s_wide;         // which kernel takes the prefix and the own parts
+  long long p_tiles, s_tiles;  // row tiles: of all groups (a bound), of an entry
+  long long rows;
   int p_chunks, s_chunks;
   size_t off_lse, bytes;
 };
@@ -531,11 +338,29 @@ int plan_sms() {
   return n;
 }
 
-// Chunks per item: enough for about three CTAs an SM, no chunk of fewer than kMinChunkPages pages.
-int plan_chunks(long long items, int tokens, int sms) {
+// Chunks per item of the thin kernel: enough for about three CTAs an SM, no
+// chunk of fewer than kMinChunkPages pages.
+int thin_chunks(long long items, int tokens, int sms) {
   const int pages = (tokens + kPage - 1) / kPage;
   const long long want = (3ll * sms + items - 1) / items;
   return static_cast<int>(std::max(1ll, std::min<long long>({want, pages / kMinChunkPages, 128})));
+}
+
+// Chunks per item of the wide kernel (one CTA an SM): the count whose waves
+// of CTAs take the least time, a CTA costing its key tiles and about three
+// more to start and to write its rows.
+int wide_chunks(long long items, int tokens, int sms) {
+  const int tiles = (tokens + 127) / 128;
+  int best = 1;
+  long long cost = INT64_MAX;
+  for (int c = 1; c <= std::min(tiles, 64); ++c) {
+    const long long t = (items * c + sms - 1) / sms * ((tiles + c - 1) / c + 3);
+    if (t < cost) {
+      cost = t;
+      best = c;
+    }
+  }
+  return best;
 }
 
 bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_prefix, int max_len, PrefixPlan* out) {
@@ -544,12 +369,16 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
   const int mp = max_prefix > 0 ? std::min(max_prefix, cap) : cap, ml = max_len > 0 ? std::min(max_len, cap) : cap;
   PrefixPlan r{};
   r.rows = static_cast<long long>(B) * T * Hq;
-  r.p_tiles = NG > 0 ? (B * tg + static_cast<long long>(NG) * (kThinRows - 1)) / kThinRows : 0;
-  r.s_tiles = (tg + kThinRows - 1) / kThinRows;
+  r.p_wide = NG > 0 && B * tg >= kWideFrom * NG;
+  r.s_wide = tg >= kWideFrom;
+  const int p_rows = r.p_wide ? kWideRows : kThinRows, s_rows = r.s_wide ? kWideRows : kThinRows;
+  r.p_tiles = NG > 0 ? (B * tg + static_cast<long long>(NG) * (p_rows - 1)) / p_rows : 0;
+  r.s_tiles = (tg + s_rows - 1) / s_rows;
   const int sms = plan_sms();
-  r.p_chunks = NG > 0 ? plan_chunks(r.p_tiles * kv.n_kv_heads, mp, sms) : 0;
-  r.s_chunks = plan_chunks(B * r.s_tiles * kv.n_kv_heads, ml, sms);
-  if ((r.p_tiles * r.p_chunks + B * r.s_tiles * r.s_chunks) * kv.n_kv_heads > INT32_MAX) return false;
+  const long long p_items = r.p_tiles * kv.n_kv_heads, s_items = B * r.s_tiles * kv.n_kv_heads;
+  r.p_chunks = NG == 0 ? 0 : r.p_wide ? wide_chunks(p_items, mp, sms) : thin_chunks(p_items, mp, sms);
+  r.s_chunks = r.s_wide ? wide_chunks(s_items, ml, sms) : thin_chunks(s_items, ml, sms);
+  if (p_items * r.p_chunks + s_items * r.s_chunks > INT32_MAX) return false;
   const int chunks = NG == 0 && r.s_chunks == 1 ? 0 : r.p_chunks + r.s_chunks;
   const size_t lse = (sizeof(float) * r.rows * chunks + 255) / 256 * 256;
   r.off_lse = 256;  // (the first 256 bytes: a status word for callers without one)
@@ -599,19 +428,29 @@ bool page_map(const dflash_paged_kv& kv, void* base, CUtensorMap* out) {
 }
 
 template <typename T16, int DH>
-cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_thin(const PrefixParams& p, long long n_prefix, long long n_own, bool behind, const CUtensorMap& tk,
+                        const CUtensorMap& tv, cudaStream_t s) {
   static FuncAttr attr;
-  cudaError_t e = attr.ensure(ThinLayout<DH>::SMEM, [](int v) {
+  const cudaError_t e = attr.ensure(ThinLayout<DH>::SMEM, [](int v) {
     return cudaFuncSetAttribute(k_prefix_thin<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
   });
   if (e != cudaSuccess) return e;
-  const long long blocks =
-      (static_cast<long long>(p.p_tiles) * p.p_chunks + static_cast<long long>(p.B) * p.s_tiles * p.s_chunks) * p.Hkv;
-  e = launch_k(k_prefix_thin<T16, DH>, dim3(static_cast<unsigned>(blocks)), dim3(kThinThreads), ThinLayout<DH>::SMEM,
-               s, dim3(1), false, tk, tv, p);
+  return launch_k(k_prefix_thin<T16, DH>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(kThinThreads),
+                  ThinLayout<DH>::SMEM, s, dim3(1), behind, tk, tv, p, static_cast<int>(n_prefix));
+}
+
+template <typename T16, int DH>
+cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int elem, const CUtensorMap& tk,
+                          const CUtensorMap& tv, cudaStream_t s) {
+  const long long n_prefix = plan.p_tiles * plan.p_chunks * p.Hkv, n_own = p.B * plan.s_tiles * plan.s_chunks * p.Hkv;
+  const long long pw = plan.p_wide ? n_prefix : 0, ow = plan.s_wide ? n_own : 0;
+  cudaError_t e = cudaSuccess;
+  if (pw + ow > 0) e = launch_prefix_wide(p, elem, DH, pw, ow, tk, tv, s);
+  if (e == cudaSuccess && n_prefix + n_own > pw + ow)
+    e = launch_thin<T16, DH>(p, n_prefix - pw, n_own - ow, pw + ow > 0, tk, tv, s);
   if (e != cudaSuccess || (p.NG == 0 && p.s_chunks == 1)) return e;
   return launch_k(k_prefix_join<T16, DH>, dim3(p.B * p.T, (p.Hq + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32),
-                  0, s, dim3(1), false, p);
+                  0, s, dim3(1), true, p);
 }
 
 }  // namespace
@@ -697,11 +536,11 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.s_chunks = plan.s_chunks;
   cudaError_t e;
   if (kv->elem == DFLASH_ELEM_BF16)
-    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, tk, tv, stream)
-                           : launch_prefix<__nv_bfloat16, 128>(p, tk, tv, stream);
+    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, plan, kv->elem, tk, tv, stream)
+                           : launch_prefix<__nv_bfloat16, 128>(p, plan, kv->elem, tk, tv, stream);
   else
-    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, tk, tv, stream)
-                           : launch_prefix<__half, 128>(p, tk, tv, stream);
+    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, plan, kv->elem, tk, tv, stream)
+                           : launch_prefix<__half, 128>(p, plan, kv->elem, tk, tv, stream);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
