@@ -10,11 +10,10 @@
 // matrix of rows), each sequence's own keys for its own rows, either of them
 // in several chunks of pages, and a last kernel joins the partial results in
 // a fixed order.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 
 #include "prefix_common.cuh"
+#include "tma_map.h"
 
 namespace dflash {
 
@@ -399,24 +398,9 @@ dflash_status check_prefix(const dflash_paged_kv* kv, int Hq, int B, int T, int 
   return DFLASH_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      ptr = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
 // Pages of one layer as a 4-D map with boxes of 16 tokens x 64 elements (128-byte swizzled rows).
 bool page_map(const dflash_paged_kv& kv, void* base, CUtensorMap* out) {
-  const auto fn = encode_fn();
+  const auto fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   const cuuint64_t dh = kv.head_dim;
   const cuuint64_t gdim[4] = {dh, kPage, static_cast<cuuint64_t>(kv.n_kv_heads), static_cast<cuuint64_t>(kv.n_pages)};
