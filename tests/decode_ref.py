@@ -154,7 +154,7 @@ def w4_values(W, scale, zero, group, fmt):
     if fmt == "e2m1":
         w = torch.tensor(E2M1 + [-x for x in E2M1], dtype=torch.float64, device=W.device)[codes]
     else:
-        z = torch.full(scale.shape, 8, device=W.device) if zero is None else zero.clamp(max=128).long()
+        z = torch.full(scale.shape, 8, device=W.device) if zero is None else zero.long()
         w = (codes - z.repeat_interleave(group, 1)[:, :K]).double()
     return w * scale.double().repeat_interleave(group, 1)[:, :K]
 
