@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
   const int pg0 = it.pg0, pg1 = it.pg1, tokens = it.tokens, kvh = it.kvh;
   const Row row[2] = {find_row(p, it, it.row0 + gr), find_row(p, it, it.row0 + gr + 8)};
 
+  const int parts = it.last && p.merge ? prefix_parts(p, it.b0) : 0;  // of the prefix, to be added at the end
+
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * kThinStages;
   uint8_t* ring = smem + warp * L::WARP;
   const int mine = pg1 > pg0 + warp ? (pg1 - pg0 - warp + kThinWarps - 1) / kThinWarps : 0;
@@ -221,6 +223,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
   }
   __syncthreads();
+  if (parts > 0) pdl_wait();
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
   const int out_chunk = it.shared ? it.chunk : p.p_chunks + it.chunk;
   for (int e = threadIdx.x; e < kThinRows * (DH / 4); e += kThinThreads) {
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     float mx = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
-    const float ms = mx == -INFINITY ? 0.f : mx;
+    float ms = mx == -INFINITY ? 0.f : mx;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
 #pragma unroll
@@ -243,10 +246,32 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
       a.z += f * v.z;
       a.w += f * v.w;
     }
+    if (parts > 0) {
+      // the prefix's partial results, in order; each is normalised by its own sum
+      float top = sum > 0.f ? ms + log2f(sum) : -INFINITY;
+      const float own = top;
+#pragma unroll 4
+      for (int c = 0; c < parts; ++c) top = fmaxf(top, p.part_lse[c * R + w.at]);
+      const float base = top == -INFINITY ? 0.f : top, f = sum > 0.f ? exp2f(own - base) / sum : 0.f;
+      a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+      float weight = exp2f(own - base);
+#pragma unroll 4
+      for (int c = 0; c < parts; ++c) {
+        const float g = exp2f(p.part_lse[c * R + w.at] - base);
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (c * R + w.at) * DH + d);
+        weight += g;
+        a.x += g * v.x;
+        a.y += g * v.y;
+        a.z += g * v.z;
+        a.w += g * v.w;
+      }
+      sum = weight;
+      ms = base;
+    }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     const float lse2 = sum > 0.f ? ms + log2f(sum) : -INFINITY;
-    if (it.whole) {
+    if (it.last) {
       *reinterpret_cast<uint2*>(static_cast<T16*>(p.out) + w.at * DH + d) = make_uint2(M::pack(a.x, a.y), M::pack(a.z, a.w));
       if (d == 0 && p.lse != nullptr) p.lse[w.at] = lse2 * 0.69314718055994531f;
     } else {
@@ -259,53 +284,60 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
 
 constexpr int kJoinWarps = 8;
 
-// out of the partial results: a warp per query row, chunks in order.
+// out of the partial results, chunks in order: `share` warps (1 or 8) a query
+// row, each adding every share-th chunk.
 template <typename T16, int DH>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, int share) {
   using M = Mma16<T16>;
   constexpr int E = DH / 32;  // elements a lane
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tok = blockIdx.x, b = tok / p.T, t = tok % p.T;
-  const int h = blockIdx.y * kJoinWarps + warp;
-  pdl_wait();
-  if (h >= p.Hq || t >= entry_rows(p, b)) return;
+  __shared__ float s_a[kJoinWarps][DH], s_sum[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % share;
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-  const long long row = static_cast<long long>(tok) * p.Hq + h;
-  int n_pre = 0;
-  if (p.NG > 0) {
-    if (bounds_ok(p)) {
-      const int pages = (find_entry(p, b).tokens + kPage - 1) / kPage, per = chunk_pages(pages, p.p_chunks);
-      n_pre = (pages + per - 1) / per;
-    } else if (tok == 0 && h == 0 && lane == 0) {
-      flag_status(p.status, ST_BAD_BLOCK);
-    }
+  const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / share) + warp / share;
+  const long long tok = row / p.Hq;
+  const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+  const bool live = row < R && t < entry_rows(p, b);
+  int n_pre = 0, n_all = 0;
+  if (live) {
+    n_pre = prefix_parts(p, b);
+    const int pages = (seq_tokens(p, p.seq != nullptr ? p.seq[b] : b) + kPage - 1) / kPage;
+    const int per = chunk_pages(pages, p.s_chunks);
+    n_all = n_pre + (pages + per - 1) / per;
   }
-  const int pages = (seq_tokens(p, p.seq != nullptr ? p.seq[b] : b) + kPage - 1) / kPage;
-  const int per = chunk_pages(pages, p.s_chunks);
-  const int n_all = n_pre + (pages + per - 1) / per;
+  pdl_wait();
   float mx = -INFINITY, sum = 0.f, a[E] = {};
   auto place = [&](int c) { return static_cast<long long>(c < n_pre ? c : p.p_chunks + c - n_pre) * R + row; };
   for (int c = lane; c < n_all; c += 32) mx = fmaxf(mx, p.part_lse[place(c)]);
   mx = warp_max(mx);
   const float ms = mx == -INFINITY ? 0.f : mx;
 #pragma unroll 4
-  for (int c = 0; c < n_all; ++c) {
+  for (int c = sub; c < n_all; c += share) {
     const long long at = place(c);
     const float f = exp2f(p.part_lse[at] - ms);
     const float* src = p.part_o + at * DH + lane * E;
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      a[0] += f * v.x;
-      a[1] += f * v.y;
-      a[2] += f * v.z;
-      a[3] += f * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      a[0] += f * v.x;
-      a[1] += f * v.y;
-    }
+    float v[E];
+    if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] += f * v[e];
     sum += f;
   }
+  if (share > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_a[warp][lane * E + e] = a[e];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = 0.f;
+    sum = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] += s_a[w][lane * E + e];
+      sum += s_sum[w];
+    }
+  }
+  if (!live) return;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   T16* dst = static_cast<T16*>(p.out) + row * DH + lane * E;
 #pragma unroll
@@ -320,7 +352,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 constexpr int kWideFrom = 48;
 
 struct PrefixPlan {
-  bool p_wide, s_wide;         // which kernel takes the prefix and the own parts
+  int p_wide, s_wide;          // row tiles (1 or 2) of the wide kernel's CTAs, 0: the thin kernel takes the part
+  bool merge;                  // own parts add the prefix's partial results
   long long p_tiles, s_tiles;  // row tiles: of all groups (a bound), of an entry
   long long rows;
   int p_chunks, s_chunks;
@@ -337,23 +370,15 @@ int plan_sms() {
   return n;
 }
 
-// Chunks per item of the thin kernel: enough for about three CTAs an SM, no
-// chunk of fewer than kMinChunkPages pages.
-int thin_chunks(long long items, int tokens, int sms) {
-  const int pages = (tokens + kPage - 1) / kPage;
-  const long long want = (3ll * sms + items - 1) / items;
-  return static_cast<int>(std::max(1ll, std::min<long long>({want, pages / kMinChunkPages, 128})));
-}
-
-// Chunks per item of the wide kernel (one CTA an SM): the count whose waves
-// of CTAs take the least time, a CTA costing its key tiles and about three
-// more to start and to write its rows.
-int wide_chunks(long long items, int tokens, int sms) {
-  const int tiles = (tokens + 127) / 128;
+// Chunks per item: the count whose waves of CTAs (`slots` at once) take the
+// least time, a CTA costing its steps (of `step` pages) and `start` more to
+// start and to write its rows, and a part in several chunks `join` more.
+int plan_chunks(long long items, int tokens, long long slots, int step, int start, int join, int most) {
+  const int steps = std::max(1, (tokens + step * kPage - 1) / (step * kPage));
   int best = 1;
   long long cost = INT64_MAX;
-  for (int c = 1; c <= std::min(tiles, 64); ++c) {
-    const long long t = (items * c + sms - 1) / sms * ((tiles + c - 1) / c + 3);
+  for (int c = 1; c <= std::min(steps, most); ++c) {
+    const long long t = (items * c + slots - 1) / slots * ((steps + c - 1) / c + start) + (c > 1 ? join : 0);
     if (t < cost) {
       cost = t;
       best = c;
@@ -363,25 +388,34 @@ int wide_chunks(long long items, int tokens, int sms) {
 }
 
 bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_prefix, int max_len, PrefixPlan* out) {
-  const long long tg = static_cast<long long>(T) * (Hq / kv.n_kv_heads);
+  const int G = Hq / kv.n_kv_heads;
+  const long long tg = static_cast<long long>(T) * G;
   const int cap = kv.max_pages * kPage;
   const int mp = max_prefix > 0 ? std::min(max_prefix, cap) : cap, ml = max_len > 0 ? std::min(max_len, cap) : cap;
   PrefixPlan r{};
   r.rows = static_cast<long long>(B) * T * Hq;
-  r.p_wide = NG > 0 && B * tg >= kWideFrom * NG;
-  r.s_wide = tg >= kWideFrom;
-  const int p_rows = r.p_wide ? kWideRows : kThinRows, s_rows = r.s_wide ? kWideRows : kThinRows;
+  const bool fits = G <= kWideTile;  // (a token's heads stay in one row tile)
+  if (fits && NG > 0 && B * tg >= static_cast<long long>(kWideFrom) * NG)
+    r.p_wide = B * tg > static_cast<long long>(wide_rows(G)) * NG ? 2 : 1;
+  if (fits && tg >= kWideFrom) r.s_wide = tg > wide_rows(G) ? 2 : 1;
+  const int p_rows = r.p_wide ? r.p_wide * wide_rows(G) : kThinRows;
+  const int s_rows = r.s_wide ? r.s_wide * wide_rows(G) : kThinRows;
   r.p_tiles = NG > 0 ? (B * tg + static_cast<long long>(NG) * (p_rows - 1)) / p_rows : 0;
   r.s_tiles = (tg + s_rows - 1) / s_rows;
-  const int sms = plan_sms();
+  const int sms = plan_sms(), thin_slots = sms * (kv.head_dim == 64 ? 4 : 2);
   const long long p_items = r.p_tiles * kv.n_kv_heads, s_items = B * r.s_tiles * kv.n_kv_heads;
-  r.p_chunks = NG == 0 ? 0 : r.p_wide ? wide_chunks(p_items, mp, sms) : thin_chunks(p_items, mp, sms);
-  r.s_chunks = r.s_wide ? wide_chunks(s_items, ml, sms) : thin_chunks(s_items, ml, sms);
+  const auto chunks = [&](int wide, long long items, int tokens, int join) {
+    return wide ? plan_chunks(items, tokens, sms * (3 - wide), kMinChunkPages, 3, join, 64)
+                : plan_chunks(items, tokens, thin_slots, kMinChunkPages, 2, join, 128);
+  };
+  r.p_chunks = NG == 0 ? 0 : chunks(r.p_wide, p_items, mp, 0);
+  r.s_chunks = chunks(r.s_wide, s_items, ml, 3);
+  // (a wide own part adds a row's copies one after the other)
+  r.merge = NG > 0 && r.s_chunks == 1 && !(r.s_wide && r.p_chunks > 4);
   if (p_items * r.p_chunks + s_items * r.s_chunks > INT32_MAX) return false;
-  const int chunks = NG == 0 && r.s_chunks == 1 ? 0 : r.p_chunks + r.s_chunks;
-  const size_t lse = (sizeof(float) * r.rows * chunks + 255) / 256 * 256;
+  const int parts = r.p_chunks + (r.merge || (NG == 0 && r.s_chunks == 1) ? 0 : r.s_chunks);
   r.off_lse = 256;  // (the first 256 bytes: a status word for callers without one)
-  r.bytes = r.off_lse + lse + sizeof(float) * r.rows * chunks * kv.head_dim;
+  r.bytes = r.off_lse + (sizeof(float) * r.rows * parts + 255) / 256 * 256 + sizeof(float) * r.rows * parts * kv.head_dim;
   *out = r;
   return true;
 }
@@ -391,9 +425,8 @@ dflash_status check_prefix(const dflash_paged_kv* kv, int Hq, int B, int T, int 
     return DFLASH_ERR_INVALID_ARG;
   if (Hq % kv->n_kv_heads) return DFLASH_ERR_INVALID_ARG;
   if (kv->elem == DFLASH_ELEM_F32 || (kv->head_dim != 64 && kv->head_dim != 128)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
-  // row counts stay well inside 32 bits, and so do the blocks of the joining kernel
-  if (static_cast<long long>(B) * T * Hq > INT32_MAX / 2 || static_cast<long long>(Hq + 7) / 8 > 65535 ||
-      NG > (1 << 20))
+  // row counts stay well inside 32 bits
+  if (static_cast<long long>(B) * T * Hq > INT32_MAX / 2 || NG > (1 << 20))
     return DFLASH_ERR_UNSUPPORTED_SHAPE;
   return DFLASH_OK;
 }
@@ -411,6 +444,21 @@ bool page_map(const dflash_paged_kv& kv, void* base, CUtensorMap* out) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as a 3-D map (elements, heads, tokens) with boxes of a row tile's
+// whole tokens x the group's heads x 64 elements.
+bool query_map(const dflash_paged_kv& kv, const void* q, int Hq, long long tokens, long long ld, CUtensorMap* out) {
+  const auto fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const int G = Hq / kv.n_kv_heads;
+  const cuuint64_t gdim[3] = {static_cast<cuuint64_t>(kv.head_dim), static_cast<cuuint64_t>(Hq),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(kv.head_dim) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kWideTile / G)}, es[3] = {1, 1, 1};
+  return fn(out, kv.elem == DFLASH_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(q), gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T16, int DH>
 cudaError_t launch_thin(const PrefixParams& p, long long n_prefix, long long n_own, bool behind, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t s) {
@@ -424,17 +472,21 @@ cudaError_t launch_thin(const PrefixParams& p, long long n_prefix, long long n_o
 }
 
 template <typename T16, int DH>
-cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int elem, const CUtensorMap& tk,
-                          const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int elem, const CUtensorMap& tq,
+                          const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   const long long n_prefix = plan.p_tiles * plan.p_chunks * p.Hkv, n_own = p.B * plan.s_tiles * plan.s_chunks * p.Hkv;
-  const long long pw = plan.p_wide ? n_prefix : 0, ow = plan.s_wide ? n_own : 0;
   cudaError_t e = cudaSuccess;
-  if (pw + ow > 0) e = launch_prefix_wide(p, elem, DH, pw, ow, tk, tv, s);
-  if (e == cudaSuccess && n_prefix + n_own > pw + ow)
-    e = launch_thin<T16, DH>(p, n_prefix - pw, n_own - ow, pw + ow > 0, tk, tv, s);
-  if (e != cudaSuccess || (p.NG == 0 && p.s_chunks == 1)) return e;
-  return launch_k(k_prefix_join<T16, DH>, dim3(p.B * p.T, (p.Hq + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32),
-                  0, s, dim3(1), true, p);
+  if (n_prefix > 0)
+    e = plan.p_wide ? launch_prefix_wide(p, elem, DH, plan.p_wide, n_prefix, 0, false, tq, tk, tv, s)
+                    : launch_thin<T16, DH>(p, n_prefix, 0, false, tk, tv, s);
+  if (e == cudaSuccess)
+    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, plan.s_wide, 0, n_own, n_prefix > 0, tq, tk, tv, s)
+                    : launch_thin<T16, DH>(p, 0, n_own, n_prefix > 0, tk, tv, s);
+  if (e != cudaSuccess || p.merge || (p.NG == 0 && p.s_chunks == 1)) return e;
+  // few rows of many parts: a row's parts over all the warps of a CTA
+  const int share = p.p_chunks + p.s_chunks >= 16 ? kJoinWarps : 1, per = kJoinWarps / share;
+  return launch_k(k_prefix_join<T16, DH>, dim3(static_cast<unsigned>((plan.rows + per - 1) / per)),
+                  dim3(kJoinWarps * 32), 0, s, dim3(1), true, p, share);
 }
 
 }  // namespace
@@ -485,11 +537,14 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   PrefixPlan plan;
   if (!make_plan(*kv, n_q_heads, B, T, NG, max_prefix, max_len, &plan)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
   if (workspace_bytes < plan.bytes) return DFLASH_ERR_WORKSPACE;
-  CUtensorMap tk, tv;
-  if (!page_map(*kv, kv->k, &tk) || !page_map(*kv, kv->v, &tv)) return DFLASH_ERR_CUDA;
+  const long long ldq = one ? qd : ld_q;
+  CUtensorMap tq{}, tk, tv;
+  if (!page_map(*kv, kv->k, &tk) || !page_map(*kv, kv->v, &tv) ||
+      ((plan.p_wide || plan.s_wide) && !query_map(*kv, q, n_q_heads, static_cast<long long>(B) * T, ldq, &tq)))
+    return DFLASH_ERR_CUDA;
   PrefixParams p{};
   p.q = q;
-  p.ld_q = one ? 0 : ld_q;
+  p.ld_q = ldq;
   p.n_rows = n_rows;
   p.seq = seq;
   p.group_off = group_off;
@@ -510,9 +565,10 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.out = out;
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  const int chunks = plan.p_chunks + plan.s_chunks;
+  p.merge = plan.merge;
+  const int parts = plan.p_chunks + (plan.merge ? 0 : plan.s_chunks);
   p.part_lse = reinterpret_cast<float*>(ws + plan.off_lse);
-  p.part_o = reinterpret_cast<float*>(ws + plan.off_lse + (sizeof(float) * plan.rows * chunks + 255) / 256 * 256);
+  p.part_o = reinterpret_cast<float*>(ws + plan.off_lse + (sizeof(float) * plan.rows * parts + 255) / 256 * 256);
   p.status = status != nullptr ? status : reinterpret_cast<int*>(ws);
   p.p_tiles = static_cast<int>(plan.p_tiles);
   p.p_chunks = plan.p_chunks;
@@ -520,11 +576,11 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.s_chunks = plan.s_chunks;
   cudaError_t e;
   if (kv->elem == DFLASH_ELEM_BF16)
-    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, plan, kv->elem, tk, tv, stream)
-                           : launch_prefix<__nv_bfloat16, 128>(p, plan, kv->elem, tk, tv, stream);
+    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, plan, kv->elem, tq, tk, tv, stream)
+                           : launch_prefix<__nv_bfloat16, 128>(p, plan, kv->elem, tq, tk, tv, stream);
   else
-    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, plan, kv->elem, tk, tv, stream)
-                           : launch_prefix<__half, 128>(p, plan, kv->elem, tk, tv, stream);
+    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, plan, kv->elem, tq, tk, tv, stream)
+                           : launch_prefix<__half, 128>(p, plan, kv->elem, tq, tk, tv, stream);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

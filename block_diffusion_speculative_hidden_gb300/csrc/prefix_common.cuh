@@ -25,6 +25,7 @@ struct PrefixParams {
   int* status;
   int p_tiles, p_chunks;  // prefix parts: row tiles over all groups (a bound), chunks of pages
   int s_tiles, s_chunks;  // own parts: row tiles of an entry, chunks of pages
+  bool merge;             // own parts (of one chunk) add the prefix's partial results and write the result
 };
 
 // Chunks are whole multiples of this many pages (a key tile of the wide
@@ -116,6 +117,13 @@ __device__ __forceinline__ Group find_entry(const PrefixParams& p, int b) {
   return Group{0, 0, -1, 0, 0};
 }
 
+// How many partial results entry b has of its prefix (the whole warp asks).
+__device__ __forceinline__ int prefix_parts(const PrefixParams& p, int b) {
+  if (p.NG == 0 || !bounds_ok(p)) return 0;
+  const int pages = (find_entry(p, b).tokens + kPage - 1) / kPage, per = chunk_pages(pages, p.p_chunks);
+  return (pages + per - 1) / per;
+}
+
 // What one CTA works on: a tile of query rows of one kv head over a chunk of pages.
 struct Item {
   bool shared;    // a group's prefix (else an entry's own sequence)
@@ -125,7 +133,7 @@ struct Item {
   int tokens;     // keys of the sequence
   int table_row;
   int pg0, pg1;   // its pages
-  bool whole;     // the only part of its rows: written as the result, even when it holds no key
+  bool last;      // an own part that writes the result, even when it holds no key
 };
 
 // Item `index` of the prefix parts (n_prefix of them come first) and own
@@ -159,6 +167,9 @@ __device__ __forceinline__ bool find_item(const PrefixParams& p, int index, int 
     it.table_row = p.seq != nullptr ? p.seq[b] : b;
     it.tokens = seq_tokens(p, it.table_row);
     it.rows = entry_rows(p, b) * p.G;
+    if (p.NG > 0 && b == 0 && it.row0 == 0 && it.kvh == 0 && it.chunk == 0 && threadIdx.x < 32 && !bounds_ok(p) &&
+        threadIdx.x == 0)
+      flag_status(p.status, ST_BAD_BLOCK);
     if (first && it.row0 == 0) {
       const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
       if (n < 0 || n > p.T) flag_status(p.status, ST_BAD_ROWS);
@@ -171,8 +182,8 @@ __device__ __forceinline__ bool find_item(const PrefixParams& p, int index, int 
   const int per = chunk_pages(pages, chunks);
   it.pg0 = it.chunk * per;
   it.pg1 = min(pages, it.pg0 + per);
-  it.whole = p.NG == 0 && p.s_chunks == 1;
-  return it.pg0 < it.pg1 || it.whole;
+  it.last = !it.shared && (p.merge || (p.NG == 0 && p.s_chunks == 1));
+  return it.pg0 < it.pg1 || it.last;
 }
 
 // A query row of an item: whether there is one, its place in q and out
@@ -236,9 +247,12 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// prefix_wide.cu: items of up to kWideRows query rows, n_prefix prefix items and then n_own own ones.
-constexpr int kWideRows = 256;
-cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, long long n_prefix, long long n_own,
-                               const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+// prefix_wide.cu: items of one or two tiles of wide_rows(G) query rows (whole
+// tokens), n_prefix prefix items or n_own own ones.
+constexpr int kWideTile = 128;  // rows of an MMA
+__host__ __device__ inline int wide_rows(int G) { return kWideTile / G * G; }
+cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, int tiles, long long n_prefix,
+                               long long n_own, bool behind, const CUtensorMap& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, cudaStream_t s);
 
 }  // namespace dflash

@@ -1,47 +1,57 @@
 // Prefix attention, items of many query rows: the fifth-generation tensor
-// cores (tcgen05) with two tiles of 128 query rows a CTA.
+// cores (tcgen05) with one or two tiles of 128 query rows a CTA.
 //
-// One warpgroup per row tile runs the softmax, a query row a thread (its
-// TMEM lane), so a row's maximum and sum never leave the thread.  Per tile of
-// 128 keys: S = Q K^T into TMEM (one MMA chain, Q and K from shared memory),
-// P = 2^(S scale - m) rounded to 16 bits over S's own columns, and O += P V
-// with P as the A operand from TMEM.  The two row tiles share the K / V
+// Per tile of 128 keys and row tile: S = Q K^T into TMEM (one MMA chain, Q and
+// K from shared memory), P = 2^(S scale - m) rounded to 16 bits over S's own
+// columns, and O += P V with P as the A operand from TMEM.  Eight warps a row
+// tile run the softmax, two threads a query row (its TMEM lane), each with
+// half of the keys and of the head's dimensions.  Two row tiles share the K / V
 // stream and alternate on the tensor pipe: while one tile's softmax runs, the
-// other tile's products do.  m moves only when a row's maximum passes it by
-// more than 2^8, and O is rescaled in TMEM only then, so P stays at most 2^8.
+// other tile's products do.  m is the maximum of a row's first tile and moves
+// (O is then rescaled in TMEM) only when a later tile's P sums to 2^14 or
+// more, so P stays within 16 bits and most tiles need no maximum.
 #include "prefix_common.cuh"
 
 namespace dflash {
 
 namespace {
 
-constexpr int kWideTile = 128;       // query rows of a tile: one TMEM lane each
 constexpr int kWideKeys = 128;       // keys of a tile
 constexpr int kWidePages = kWideKeys / kPage;
-constexpr int kWideThreads = 384;    // two softmax warpgroups; the TMA warp, the MMA warp and two that only share registers
-// registers a thread: 3 * 168 at launch, given to the softmax (224 + 224 + 56 = 3 * 168)
-constexpr int kWideSoftRegs = 224, kWideFeedRegs = 56;
-constexpr float kWideLazy = 8.f;     // how far (in powers of two) a maximum may pass m
+constexpr int kWideLazy = 14;        // how far (in powers of two) a tile's P may sum up before m moves
 
-template <int DH>
+// NT row tiles.  Two take all of an SM (TMEM: two S and two O); with one, two
+// CTAs share an SM, so that one's start and end run beside the other's middle.
+template <int DH, int NT>
 struct WideLayout {
+  static constexpr int SOFT = 8 * NT;                       // softmax warps; then the TMA warp, the MMA warp and
+  static constexpr int THREADS = (SOFT + 4) * 32;           // two warps that only hand their registers on
+  // registers a thread: at launch, and after the warps' exchange
+  static constexpr int REGS = NT == 2 ? 96 : 80;
+  static constexpr int SOFT_REGS = NT == 2 ? 112 : 104, FEED_REGS = 32;
+  static_assert(SOFT * SOFT_REGS + 4 * FEED_REGS <= (SOFT + 4) * REGS, "the exchange stays within the launch's registers");
   static constexpr int NCH = DH / 64;                       // 128-byte column chunks of a head
   static constexpr int Q_CH = kWideTile * 128;
   static constexpr int Q_TILE = NCH * Q_CH;
   static constexpr int KV_CH = kWideKeys * 128;
   static constexpr int SLOT = NCH * KV_CH;                  // a K or a V tile
-  static constexpr int NS = DH == 128 ? 5 : 8;              // ring slots: K(0), V(0), K(1), ..
-  static constexpr int OFF_KV = 2 * Q_TILE;
-  static constexpr int OFF_BAR = OFF_KV + NS * SLOT;
-  static constexpr int BYTES = OFF_BAR + 256;
-  static constexpr int SMEM = 1024 + BYTES;
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * kWideKeys;  // TMEM: two S (and P), two O
-  static constexpr uint32_t COLS = 512;
-  static_assert(O_COL + 2 * DH <= COLS, "the accumulators fit TMEM");
-  static_assert(SMEM <= 232448, "shared memory of a CTA");
-  static_assert((2 * NS + 9) * 8 + 8 <= 256, "barriers fit their area");
-  // one CTA an SM: its TMEM allocation never waits for another's
-  static_assert(2 * SMEM > 233472, "two CTAs of the kernel never share an SM");
+  static constexpr int NS = DH == 128 ? (NT == 2 ? 4 : 2) : (NT == 2 ? 8 : 5);  // ring slots: K(0), V(0), K(1), ..
+  static constexpr int OFF_KV = NT * Q_TILE;
+  static constexpr int OFF_RED = OFF_KV + NS * SLOT;        // [2][warp][lane] row maxima, sums
+  static constexpr int OFF_BAR = OFF_RED + 2 * SOFT * 32 * 4;
+  static constexpr int SMEM = 1024 + OFF_BAR + 256;
+  static constexpr uint32_t S_COL = 0, O_COL = NT * kWideKeys;  // TMEM: S (and P) of every row tile, then O
+  static constexpr uint32_t COLS = NT * 256;
+  static_assert(O_COL + NT * DH <= COLS, "the accumulators fit TMEM");
+  static_assert(SMEM <= (NT == 2 ? 232448 : 115712), "shared memory of a CTA");
+  static_assert((2 * NS + 5 * NT) * 8 + 8 <= 256, "barriers fit their area");
+  // the CTAs that an SM can hold by their shared memory find room in its 512
+  // TMEM columns: an allocation never waits for another CTA's
+  static_assert((512 / COLS + 1) * (SMEM + 1024) > 233472, "no more CTAs an SM than TMEM has room for");
+  // at the end Q and the ring stage the output rows (fp32, or 16 bits)
+  static constexpr int PITCH = DH * 4 + 16;
+  static constexpr int STAGE = kWideTile * PITCH;
+  static_assert(NT * STAGE <= OFF_RED, "the staged rows fit");
 };
 
 template <int N>
@@ -52,7 +62,26 @@ template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-
+// One thread of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+  return is != 0;
+}
+__device__ __forceinline__ void wide_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Whether v holds for any of the 64 threads that meet at the barrier.
+__device__ __forceinline__ bool wide_any(int id, bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(v ? 1 : 0), "r"(id)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ float wide_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -63,6 +92,18 @@ __device__ __forceinline__ float wide_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(token), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_store_row(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Instruction descriptor of tcgen05.mma kind::f16 with fp32 accumulators: A
 // and B fp16 or bf16, B transposed (its N dimension contiguous) for P V.
@@ -71,57 +112,63 @@ __device__ __forceinline__ constexpr uint32_t wide_idesc(int m, int n, bool b_mn
   return mma_idesc_f16_f32(m, n, b_mn) | (std::is_same<T16, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u);
 }
 
-template <typename T16, int DH>
-__global__ void __launch_bounds__(kWideThreads, 1) k_prefix_wide(const __grid_constant__ CUtensorMap tmK,
-                                                                 const __grid_constant__ CUtensorMap tmV,
-                                                                 const __grid_constant__ PrefixParams p, int n_prefix) {
-  using L = WideLayout<DH>;
+template <typename T16, int DH, int NT>
+__global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
+    k_prefix_wide(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p, int n_prefix) {
+  using L = WideLayout<DH, NT>;
   using M16 = Mma16<T16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(smem + L::OFF_RED);
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* kv_empty = kv_full + L::NS;
-  uint64_t* q_full = kv_empty + L::NS;  // [2]: per row tile, like the next three
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* q_full = kv_empty + L::NS;  // [NT]: per row tile, like the next four
+  uint64_t* s_full = q_full + NT;
+  uint64_t* p_full = s_full + NT;
+  uint64_t* o_full = p_full + NT;
+  uint64_t* part_full = o_full + NT;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_full + NT);
+  // (through a shuffle, so that what follows from it is known to be alike in a warp)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  constexpr int kTmaWarp = L::SOFT, kMmaWarp = L::SOFT + 1;
 
   pdl_trigger();  // (the kernels behind wait for this one's results on their own)
+  const int rows_tile = wide_rows(p.G);
   Item it;
-  if (!find_item(p, blockIdx.x, n_prefix, kWideRows, it)) return;
+  if (!find_item(p, blockIdx.x, n_prefix, NT * rows_tile, it)) return pdl_wait();
   const int np = max(0, it.pg1 - it.pg0);
-  const int n = (np + kWidePages - 1) / kWidePages;                 // key tiles
-  const int nt = it.rows - it.row0 > kWideTile ? 2 : 1;             // row tiles
+  const int n = (np + kWidePages - 1) / kWidePages;                    // key tiles
+  const int nt = NT == 2 && it.rows - it.row0 > rows_tile ? 2 : 1;     // row tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::NS; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&q_full[t], kWideTile);
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(&q_full[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], kWideTile);
+      mbar_init(&p_full[t], 256);
       mbar_init(&o_full[t], 1);
+      mbar_init(&part_full[t], kWideTile);
     }
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, L::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp >= 8) {
-    regs_down<kWideFeedRegs>();
-    if (warp == 8) {
-      // ---------------- K and V tiles: lane l fetches chunk l % NCH of page l / NCH
+  if (warp >= L::SOFT) {
+    regs_down<L::FEED_REGS>();
+    if (warp == kTmaWarp) {
+      // ---------------- Q, then K and V tiles: lane l fetches chunk l % NCH of page l / NCH
       const int32_t* table = p.page_table + static_cast<long long>(it.table_row) * p.max_pages + it.pg0;
       const int pg = lane / L::NCH, c = lane % L::NCH;
       auto page_id = [&](int j) {
@@ -138,6 +185,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_prefix_wide(const __grid_co
       };
       int next = n > 0 ? page_id(0) : 0, issued = 0;
       bool ok = true;
+      if (lane == 0 && n > 0) {
+        // whole tokens: a tile's first row is a token's first head of the group
+        const int token = it.b0 * p.T + it.row0 / p.G, tokens = kWideTile / p.G;
+        for (int t = 0; t < nt; ++t) {
+          mbar_arrive_expect_tx(&q_full[t], rows_tile * L::NCH * 128);
+          for (int cc = 0; cc < L::NCH; ++cc)
+            tma_rows(smem_u32(smem + t * L::Q_TILE + cc * L::Q_CH), &tmQ, &q_full[t], cc * 64, it.kvh * p.G,
+                     token + t * tokens);
+        }
+      }
       for (int j = 0; ok && j < n; ++j) {
         const int id = next, npb = min(kWidePages, np - j * kWidePages);
         if (j + 1 < n) next = page_id(j + 1);
@@ -157,71 +214,88 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_prefix_wide(const __grid_co
         }
       }
       // every copy has landed before the CTA may leave
+      if (lane == 0 && n > 0)
+        for (int t = 0; t < nt; ++t) mbar_wait(&q_full[t], 0, p.status);
       for (int i = max(0, issued - L::NS); i < issued; ++i) mbar_wait(&kv_full[i % L::NS], (i / L::NS) & 1, p.status);
-    } else if (warp == 9) {
+    } else if (warp == kMmaWarp) {
       // ---------------- MMAs.  S(j + 1) of a row tile overwrites its P(j), so
-      // it waits for P(j) V; the other row tile's products fill that time.
-      if (lane == 0 && n > 0) {
-        const uint32_t q0 = smem_u32(smem), kv0 = smem_u32(smem + L::OFF_KV);
-        auto kv_wait = [&](int i) { return mbar_wait(&kv_full[i % L::NS], (i / L::NS) & 1, p.status); };
-        auto issue_s = [&](int t, int j) {
-          const uint32_t a = q0 + t * L::Q_TILE, k = kv0 + ((2 * j) % L::NS) * L::SLOT;
-          const uint32_t id = wide_idesc<T16>(kWideTile, 16 * min(kWidePages, np - j * kWidePages), false);
+      // it waits for P(j) V; the other row tile's products fill that time.  The
+      // whole warp walks along and one thread issues: the operands are then
+      // uniform values (computed by that thread alone, each of them crosses
+      // over to the uniform registers on its own, 110 cycles an MMA of 64).
+      const int key_tiles = __shfl_sync(0xffffffffu, n, 0), pages = __shfl_sync(0xffffffffu, np, 0);
+      const int row_tiles = __shfl_sync(0xffffffffu, nt, 0);
+      const bool elected = elect_one();
+      const uint64_t qd = sw128_desc(smem_u32(smem), 16, 1024), kd = sw128_desc(smem_u32(smem + L::OFF_KV), 16, 1024);
+      const uint64_t vd = sw128_desc(smem_u32(smem + L::OFF_KV), L::KV_CH, 1024);
+      auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+      auto kv_wait = [&](int i) { return all(mbar_wait_spin(&kv_full[i % L::NS], (i / L::NS) & 1, p.status)); };
+      // (a descriptor's address field counts 16 bytes)
+      auto issue_s = [&](int t, int j) {
+        const uint64_t a = qd + t * (L::Q_TILE >> 4), k = kd + (2 * j) % L::NS * (L::SLOT >> 4);
+        const uint32_t id = wide_idesc<T16>(kWideTile, 16 * min(kWidePages, pages - j * kWidePages), false);
+        if (elected) {
 #pragma unroll
           for (int ks = 0; ks < DH / 16; ++ks)
-            tc_mma_bf16(tmem + L::S_COL + t * kWideKeys, sw128_desc(a + (ks >> 2) * L::Q_CH + (ks & 3) * 32, 16, 1024),
-                        sw128_desc(k + (ks >> 2) * L::KV_CH + (ks & 3) * 32, 16, 1024), id, ks > 0 ? 1u : 0u);
+            tc_mma_bf16(tmem + L::S_COL + t * kWideKeys, a + ((ks >> 2) * L::Q_CH + (ks & 3) * 32 >> 4),
+                        k + ((ks >> 2) * L::KV_CH + (ks & 3) * 32 >> 4), id, ks > 0 ? 1u : 0u);
           tc_commit(&s_full[t]);
-          if (t == nt - 1) tc_commit(&kv_empty[(2 * j) % L::NS]);
-        };
-        bool ok = kv_wait(0);
-        for (int t = 0; ok && t < nt; ++t) {
-          ok = mbar_wait(&q_full[t], 0, p.status);
-          tc_fence_after();
-          if (ok) issue_s(t, 0);
+          if (t == row_tiles - 1) tc_commit(&kv_empty[(2 * j) % L::NS]);
         }
-        for (int j = 0; ok && j < n; ++j) {
-          const int npb = min(kWidePages, np - j * kWidePages);
-          const uint32_t v = kv0 + ((2 * j + 1) % L::NS) * L::SLOT;
-          ok = kv_wait(2 * j + 1);
-          for (int t = 0; ok && t < nt; ++t) {
-            ok = mbar_wait(&p_full[t], j & 1, p.status);
-            if (!ok) break;
+        __syncwarp();
+      };
+      auto issue_o = [&](int t, int j) {
+        const uint64_t v = vd + (2 * j + 1) % L::NS * (L::SLOT >> 4);
+        const int npb = min(kWidePages, pages - j * kWidePages);
+        const uint32_t id = wide_idesc<T16>(kWideTile, DH, true);
+        if (elected) {
+#pragma unroll
+          for (int ks = 0; ks < kWidePages; ++ks)
+            if (ks < npb)
+              tc_mma_bf16_ts(tmem + L::O_COL + t * DH, tmem + L::S_COL + t * kWideKeys + 16 * ks, v + ks * (2048 >> 4), id,
+                             (j | ks) > 0 ? 1u : 0u);
+          tc_commit(&o_full[t]);
+          if (t == row_tiles - 1) tc_commit(&kv_empty[(2 * j + 1) % L::NS]);
+        }
+        __syncwarp();
+      };
+      bool ok = key_tiles > 0 && kv_wait(0);
+      for (int t = 0; ok && t < row_tiles; ++t) {
+        ok = all(mbar_wait_spin(&q_full[t], 0, p.status));
+        tc_fence_after();
+        if (ok) issue_s(t, 0);
+      }
+      for (int j = 0; ok && j < key_tiles; ++j) {
+        ok = kv_wait(2 * j + 1);
+        for (int t = 0; ok && t < row_tiles; ++t) {
+          ok = all(mbar_wait_spin(&p_full[t], j & 1, p.status));
+          tc_fence_after();
+          if (!ok) break;
+          issue_o(t, j);
+          if (j + 1 < key_tiles) {
+            ok = (t > 0 || kv_wait(2 * j + 2)) && all(mbar_wait_spin(&o_full[t], j & 1, p.status));
             tc_fence_after();
-            const uint32_t id = wide_idesc<T16>(kWideTile, DH, true);
-            for (int ks = 0; ks < npb; ++ks)
-              tc_mma_bf16_ts(tmem + L::O_COL + t * DH, tmem + L::S_COL + t * kWideKeys + 8 * ks,
-                             sw128_desc(v + ks * 2048, L::KV_CH, 1024), id, (j | ks) > 0 ? 1u : 0u);
-            tc_commit(&o_full[t]);
-            if (t == nt - 1) tc_commit(&kv_empty[(2 * j + 1) % L::NS]);
-            if (j + 1 < n) {
-              ok = (t > 0 || kv_wait(2 * j + 2)) && mbar_wait(&o_full[t], j & 1, p.status);
-              tc_fence_after();
-              if (ok) issue_s(t, j + 1);
-            }
+            if (ok) issue_s(t, j + 1);
           }
         }
       }
-      __syncwarp();
     }
-  } else if (warp < 4 * nt) {
-    regs_up<kWideSoftRegs>();
-    // ---------------- softmax: thread r of warpgroup t owns row r of tile t
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
-    const Row row = find_row(p, it, it.row0 + t * kWideTile + r);
-    {
-      const uint4* src =
-          reinterpret_cast<const uint4*>(static_cast<const T16*>(p.q) + row.token * p.ld_q + (row.at - row.token * p.Hq) * DH);
-      uint8_t* dst = smem + t * L::Q_TILE + r * 128;
-#pragma unroll
-      for (int u = 0; u < DH / 8; ++u)
-        *reinterpret_cast<uint4*>(dst + (u >> 3) * L::Q_CH + (((u & 7) ^ (r & 7)) << 4)) =
-            row.live ? src[u] : make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      mbarrier_arrive_one(&q_full[t]);
-    }
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + L::S_COL + t * kWideKeys, o_at = tmem + lanes + L::O_COL + t * DH;
+  } else if (warp < 8 * nt) {
+    regs_up<L::SOFT_REGS>();
+    // ---------------- softmax: threads r of the two halves of row tile t own row r
+    const int t = warp >> 3, quad = warp & 3, half = warp >> 2 & 1, r = quad * 32 + lane;
+    const int pair = 1 + t * 4 + quad;  // the named barrier of the row's two warps
+    Row row = find_row(p, it, it.row0 + t * rows_tile + r);
+    row.live = row.live && r < rows_tile;
+    const int parts = it.last && p.merge ? prefix_parts(p, it.b0) : 0;  // of the prefix, to be added at the end
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_at = tmem + lanes + L::S_COL + t * kWideKeys + 64 * half;
+    const uint32_t o_at = tmem + lanes + L::O_COL + t * DH + DH / 2 * half;
+    auto partner = [&](int slot, float v) {  // the other half's value
+      red[(slot * L::SOFT + warp) * 32 + lane] = v;
+      wide_bar(pair, 64);
+      return red[(slot * L::SOFT + (warp ^ 4)) * 32 + lane];
+    };
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -230,76 +304,91 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_prefix_wide(const __grid_co
       ok = ok && mbar_wait(&s_full[t], j & 1, p.status);
       __syncwarp();
       tc_fence_after();
-      uint32_t sv[kWidePages][16];
+      uint32_t sv[4][16];
 #pragma unroll
-      for (int g = 0; g < kWidePages; ++g)
-        if (g < npb) tc_ld_32x32b_x16_nw(s_at + 16 * g, sv[g]);
+      for (int g = 0; g < 4; ++g)
+        if (4 * half + g < npb) tc_ld_32x32b_x16_nw(s_at + 16 * g, sv[g]);
       tc_wait_ld();
-      // keys of the tile that this row sees (the chunk may end inside the tile)
-      const int lim = min(row.seen, it.pg1 * kPage) - key0;
-      if (__any_sync(0xffffffffu, lim < kWideKeys)) {
+      // keys of this half that the row sees (the chunk may end inside the tile)
+      const int lim = min(row.seen, it.pg1 * kPage) - key0 - 64 * half;
+      if (__any_sync(0xffffffffu, lim < 64)) {
 #pragma unroll
-        for (int g = 0; g < kWidePages; ++g)
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (g * 16 + k >= lim) sv[g][k] = 0xff800000u;  // -infinity
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto row_top = [&]() {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int g = 0; g < kWidePages; ++g)
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int k = 0; k < 16; k += 8)
+          for (int k = 0; k < 16; k += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = wide_max3(mx[e], __uint_as_float(sv[g][k + 2 * e]), __uint_as_float(sv[g][k + 2 * e + 1]));
-      const float cand = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-      const bool move = cand > m + kWideLazy;
-      if (__any_sync(0xffffffffu, move)) {
-        const float al = move ? wide_ex2(m - cand) : 1.f;  // (m = -infinity: 0)
-        if (move) m = cand;
-        l *= al;
-        if (j > 0) {
+            for (int e = 0; e < 4; ++e)
+              mx[e] = wide_max3(mx[e], __uint_as_float(sv[g][k + 2 * e]), __uint_as_float(sv[g][k + 2 * e + 1]));
+        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      };
+      // P against m, over the first half of each page's own columns; returns its sum
+      auto make_p = [&]() {
+        const float mu = m == -INFINITY ? 0.f : m;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), mneg2 = make_float2(-mu, -mu);
+        float2 sum[2] = {};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(sv[g][2 * k]), __uint_as_float(sv[g][2 * k + 1])), sc2, mneg2);
+            const float2 e = make_float2(wide_ex2(x.x), wide_ex2(x.y));
+            sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+            pk[k] = M16::pack(e.x, e.y);
+          }
+          tc_st_32x32b_x8(s_at + 16 * g, pk);
+        }
+        return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      };
+      if (j == 0) {
+        float top = row_top();
+        top = fmaxf(top, partner(0, top));
+        m = top * p.scale_log2;
+        l = make_p();
+      } else {
+        // P against the m so far.  Its sum shows whether m still serves: below
+        // 2^kWideLazy no term has grown past 16 bits.  Only where a row of the
+        // two warps fails that (an infinity or NaN included) the maxima are
+        // taken, m moves and P is made again.
+        const float sum = make_p();
+        if (!wide_any(pair, !(sum < static_cast<float>(1 << kWideLazy)) || m == -INFINITY)) {
+          l += sum;
+        } else {
+          float top = row_top();
+          top = fmaxf(top, partner(j & 1, top));
+          const float cand = fmaxf(m, top * p.scale_log2);
+          const float al = cand > m ? wide_ex2(m - cand) : 1.f;  // (m = -infinity: 0)
+          m = cand;
           // S(j) was issued after P(j - 1) V was done, so O is at rest
 #pragma unroll
-          for (int d = 0; d < DH; d += 32) {
-            uint32_t v0[16], v1[16];
-            tc_ld_32x32b_x16_nw(o_at + d, v0);
-            tc_ld_32x32b_x16_nw(o_at + d + 16, v1);
+          for (int d = 0; d < DH / 2; d += 16) {
+            uint32_t v[16];
+            tc_ld_32x32b_x16_nw(o_at + d, v);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              v0[e] = __float_as_uint(__uint_as_float(v0[e]) * al);
-              v1[e] = __float_as_uint(__uint_as_float(v1[e]) * al);
-            }
-            tc_st_32x32b_x16(o_at + d, v0);
-            tc_st_32x32b_x16(o_at + d + 16, v1);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+            tc_st_32x32b_x16(o_at + d, v);
           }
+          tc_wait_st();  // (the first P has landed before it is written again)
+          l = l * al + make_p();
         }
       }
-      const float mu = m == -INFINITY ? 0.f : m;
-      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), mneg2 = make_float2(-mu, -mu);
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int g = 0; g < kWidePages; ++g) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 x = __ffma2_rn(
-              make_float2(__uint_as_float(sv[g][2 * k]), __uint_as_float(sv[g][2 * k + 1])), sc2, mneg2);
-          const float2 e = make_float2(wide_ex2(x.x), wide_ex2(x.y));
-          sum = __fadd2_rn(sum, e);
-          pk[k] = M16::pack(e.x, e.y);
-        }
-        tc_st_32x32b_x8(s_at + 8 * g, pk);
-      }
-      l += sum.x + sum.y;
       if (key0 + npb * kPage > it.tokens) {
         // the last page is partial: what its V rows hold past the last token
         // meets probabilities of zero and must be finite
         const int i = 2 * j + 1, first = it.tokens - (key0 + (npb - 1) * kPage);
         ok = ok && mbar_wait(&kv_full[i % L::NS], (i / L::NS) & 1, p.status);
         uint8_t* v = smem + L::OFF_KV + (i % L::NS) * L::SLOT + (npb - 1) * 2048;
-        for (int e = r; e < (kPage - first) * L::NCH * 8; e += kWideTile) {
+        for (int e = half * kWideTile + r; e < (kPage - first) * L::NCH * 8; e += 2 * kWideTile) {
           const int c = e / ((kPage - first) * 8), f = e % ((kPage - first) * 8);
           *reinterpret_cast<uint4*>(v + c * L::KV_CH + first * 128 + f * 16) = make_uint4(0, 0, 0, 0);
         }
@@ -309,70 +398,130 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_prefix_wide(const __grid_co
       tc_fence_before();
       mbarrier_arrive_one(&p_full[t]);
     }
-    if (n > 0) ok = ok && mbar_wait(&o_full[t], (n - 1) & 1, p.status);
+    // the last product of every row tile: then O is whole, and Q and the ring are free
+    if (n > 0)
+      for (int q = 0; q < nt; ++q) ok = ok && mbar_wait(&o_full[q], (n - 1) & 1, p.status);
     __syncwarp();
     tc_fence_after();
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-    const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-    const long long part = (it.shared ? it.chunk : p.p_chunks + it.chunk) * R + row.at;
+    l += partner(n & 1, l);
+    float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+    float x[DH / 2];  // the row's result, this half's dimensions
+    {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int d = 0; d < DH; d += 16) {
-      uint32_t v[16];
-      if (n > 0) {
-        tc_ld_32x32b_x16_nw(o_at + d, v);
-        tc_wait_ld();
-      }
-      float x[16];
+      for (int d = 0; d < DH / 2; d += 16) {
+        uint32_t v[16];
+        if (n > 0) {
+          tc_ld_32x32b_x16_nw(o_at + d, v);
+          tc_wait_ld();
+        }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = l > 0.f ? __uint_as_float(v[e]) * inv : 0.f;
-      if (row.live && it.whole) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T16*>(p.out) + row.at * DH + d);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          dst[e] = make_uint4(M16::pack(x[8 * e], x[8 * e + 1]), M16::pack(x[8 * e + 2], x[8 * e + 3]),
-                              M16::pack(x[8 * e + 4], x[8 * e + 5]), M16::pack(x[8 * e + 6], x[8 * e + 7]));
-      } else if (row.live) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + part * DH + d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        for (int e = 0; e < 16; ++e) x[d + e] = l > 0.f ? __uint_as_float(v[e]) * inv : 0.f;
       }
     }
-    if (row.live && it.whole) {
-      if (p.lse != nullptr) p.lse[row.at] = lse2 * 0.69314718055994531f;
-    } else if (row.live) {
-      p.part_lse[part] = lse2;
+    const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
+    uint8_t* stage = smem + t * L::STAGE + r * L::PITCH;
+    if (it.last && parts > 0) {
+      // add the prefix's partial results, a copy of the row at a time (in order)
+      pdl_wait();
+      float weight = 1.f;
+      for (int c = 0; c < parts; ++c) {
+        if (half == 0) {
+          if (row.live) {
+            mbar_arrive_expect_tx(&part_full[t], DH * 4);
+            bulk_load_global(smem_u32(stage), p.part_o + (c * R + row.at) * DH, DH * 4, &part_full[t]);
+          } else {
+            mbarrier_arrive_one(&part_full[t]);
+          }
+        }
+        const float other = row.live ? p.part_lse[c * R + row.at] : -INFINITY;
+        const float top = fmaxf(lse2, other), base = top == -INFINITY ? 0.f : top;
+        const float f0 = wide_ex2(lse2 - base), f1 = wide_ex2(other - base);
+        ok = ok && mbar_wait(&part_full[t], c & 1, p.status);
+#pragma unroll
+        for (int d = 0; d < DH / 2; d += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(stage + (DH / 2 * half + d) * 4);
+          x[d] = x[d] * f0 + (f1 > 0.f ? y.x * f1 : 0.f);
+          x[d + 1] = x[d + 1] * f0 + (f1 > 0.f ? y.y * f1 : 0.f);
+          x[d + 2] = x[d + 2] * f0 + (f1 > 0.f ? y.z * f1 : 0.f);
+          x[d + 3] = x[d + 3] * f0 + (f1 > 0.f ? y.w * f1 : 0.f);
+        }
+        // (x and weight are relative to 2^top; the first term's weight is 1 where it has any)
+        weight = (lse2 > -INFINITY ? weight * f0 : 0.f) + f1;
+        lse2 = top;
+        fence_proxy_async_smem();
+        wide_bar(pair, 64);  // both halves are through with the copy
+      }
+      const float inv = weight > 0.f ? 1.f / weight : 0.f;
+#pragma unroll
+      for (int d = 0; d < DH / 2; ++d) x[d] *= inv;
+      lse2 = weight > 0.f ? lse2 + log2f(weight) : -INFINITY;
+    }
+    if (it.last) {
+#pragma unroll
+      for (int d = 0; d < DH / 2; d += 8)
+        *reinterpret_cast<uint4*>(stage + (DH / 2 * half + d) * 2) =
+            make_uint4(M16::pack(x[d], x[d + 1]), M16::pack(x[d + 2], x[d + 3]), M16::pack(x[d + 4], x[d + 5]),
+                       M16::pack(x[d + 6], x[d + 7]));
+    } else {
+#pragma unroll
+      for (int d = 0; d < DH / 2; d += 4)
+        *reinterpret_cast<float4*>(stage + (DH / 2 * half + d) * 4) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
+    }
+    fence_proxy_async_smem();
+    wide_bar(pair, 64);
+    if (row.live && half == 0) {
+      const long long part = (it.shared ? it.chunk : p.p_chunks + it.chunk) * R + row.at;
+      if (it.last) {
+        bulk_store_row(static_cast<T16*>(p.out) + row.at * DH, smem_u32(stage), DH * 2);
+        if (p.lse != nullptr) p.lse[row.at] = lse2 * 0.69314718055994531f;
+      } else {
+        bulk_store_row(p.part_o + part * DH, smem_u32(stage), DH * 4);
+        p.part_lse[part] = lse2;
+      }
+      bulk_commit();
+      bulk_wait_all();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, L::COLS);
   }
+  pdl_wait();  // (the joining kernel behind starts once all of this one has left)
+}
+
+template <typename T16, int DH, int NT>
+cudaError_t launch_wide_t(const PrefixParams& p, long long n_prefix, long long n_own, bool behind,
+                          const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  using L = WideLayout<DH, NT>;
+  static FuncAttr attr;
+  const cudaError_t e = attr.ensure(L::SMEM, [](int v) {
+    return cudaFuncSetAttribute(k_prefix_wide<T16, DH, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_k(k_prefix_wide<T16, DH, NT>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(L::THREADS), L::SMEM,
+                  s, dim3(1), behind, tq, tk, tv, p, static_cast<int>(n_prefix));
 }
 
 template <typename T16, int DH>
-cudaError_t launch_wide_t(const PrefixParams& p, long long n_prefix, long long n_own, const CUtensorMap& tk,
-                          const CUtensorMap& tv, cudaStream_t s) {
-  static FuncAttr attr;
-  const cudaError_t e = attr.ensure(WideLayout<DH>::SMEM, [](int v) {
-    return cudaFuncSetAttribute(k_prefix_wide<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
-  });
-  if (e != cudaSuccess) return e;
-  return launch_k(k_prefix_wide<T16, DH>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(kWideThreads),
-                  WideLayout<DH>::SMEM, s, dim3(1), false, tk, tv, p, static_cast<int>(n_prefix));
+cudaError_t launch_wide_n(const PrefixParams& p, int tiles, long long n_prefix, long long n_own, bool behind,
+                          const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  return tiles == 2 ? launch_wide_t<T16, DH, 2>(p, n_prefix, n_own, behind, tq, tk, tv, s)
+                    : launch_wide_t<T16, DH, 1>(p, n_prefix, n_own, behind, tq, tk, tv, s);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, long long n_prefix, long long n_own,
-                               const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, int tiles, long long n_prefix,
+                               long long n_own, bool behind, const CUtensorMap& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, cudaStream_t s) {
   if (elem == DFLASH_ELEM_BF16)
-    return head_dim == 64 ? launch_wide_t<__nv_bfloat16, 64>(p, n_prefix, n_own, tk, tv, s)
-                          : launch_wide_t<__nv_bfloat16, 128>(p, n_prefix, n_own, tk, tv, s);
-  return head_dim == 64 ? launch_wide_t<__half, 64>(p, n_prefix, n_own, tk, tv, s)
-                        : launch_wide_t<__half, 128>(p, n_prefix, n_own, tk, tv, s);
+    return head_dim == 64 ? launch_wide_n<__nv_bfloat16, 64>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s)
+                          : launch_wide_n<__nv_bfloat16, 128>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s);
+  return head_dim == 64 ? launch_wide_n<__half, 64>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s)
+                        : launch_wide_n<__half, 128>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s);
 }
 
 }  // namespace dflash
