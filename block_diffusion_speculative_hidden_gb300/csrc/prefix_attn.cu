@@ -36,6 +36,7 @@ constexpr int kThinWarps = 4;
 constexpr int kThinThreads = kThinWarps * 32;
 constexpr int kThinRows = 16;   // query rows of a tile (one MMA's rows)
 constexpr int kThinStages = 3;  // pages in flight per warp
+constexpr int kMaxParts = 128;  // chunks of a prefix
 
 template <int DH>
 struct ThinLayout {
@@ -44,7 +45,10 @@ struct ThinLayout {
   static constexpr int WARP = kThinStages * STAGE;
   static constexpr int LDO = DH + 8;                      // floats per row of a warp's partial output
   static constexpr int OFF_ML = kThinWarps * WARP;        // [warps][16][2] maxima and sums
-  static constexpr int OFF_BAR = OFF_ML + kThinWarps * kThinRows * 8;
+  static constexpr int OFF_TOP = OFF_ML + kThinWarps * kThinRows * 8;  // [16] what the weights are relative to
+  static constexpr int OFF_W = kThinRows * LDO * 4;       // weights of four rows' parts, in each warp's ring
+  static_assert(OFF_W + 4 * kMaxParts * 4 <= WARP, "the weights fit beside a warp's partial output");
+  static constexpr int OFF_BAR = OFF_TOP + kThinRows * 4;
   static constexpr int BYTES = OFF_BAR + kThinWarps * kThinStages * 8;
   static constexpr int SMEM = 1024 + BYTES;
   static_assert(kThinRows * LDO * 4 <= WARP, "a warp's partial output fits its ring");
@@ -223,17 +227,46 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
   }
   __syncthreads();
-  if (parts > 0) pdl_wait();
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
   const int out_chunk = it.shared ? it.chunk : p.p_chunks + it.chunk;
+  // weights of the prefix's partial results (each is normalised by its own
+  // sum), eight threads a row, in the unused part of the rings
+  auto weights = [&](int r) { return reinterpret_cast<float*>(smem + r / 4 * L::WARP + L::OFF_W) + r % 4 * kMaxParts; };
+  if (parts > 0) {
+    pdl_wait();
+    const int r = threadIdx.x / 8;
+    const Row w = find_row(p, it, it.row0 + r);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
+    float top = mx;
+    if (w.live)
+      for (int c = threadIdx.x % 8; c < parts; c += 8) {
+        const float v = p.part_lse[c * R + w.at];
+        weights(r)[c] = v;
+        top = fmaxf(top, v);
+      }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    if (w.live)
+      for (int c = threadIdx.x % 8; c < parts; c += 8) weights(r)[c] = exp2f(weights(r)[c] - base);
+    if (threadIdx.x % 8 == 0) reinterpret_cast<float*>(smem + L::OFF_TOP)[r] = base;
+    __syncthreads();
+  }
   for (int e = threadIdx.x; e < kThinRows * (DH / 4); e += kThinThreads) {
     const int r = e / (DH / 4), d = (e % (DH / 4)) * 4;
     const Row w = find_row(p, it, it.row0 + r);
     if (!w.live) continue;
-    float mx = -INFINITY;
+    float ms;
+    if (parts > 0) {
+      ms = reinterpret_cast<const float*>(smem + L::OFF_TOP)[r];
+    } else {
+      float mx = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
-    float ms = mx == -INFINITY ? 0.f : mx;
+      for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
+      ms = mx == -INFINITY ? 0.f : mx;
+    }
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
 #pragma unroll
@@ -246,27 +279,16 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
       a.z += f * v.z;
       a.w += f * v.w;
     }
-    if (parts > 0) {
-      // the prefix's partial results, in order; each is normalised by its own sum
-      float top = sum > 0.f ? ms + log2f(sum) : -INFINITY;
-      const float own = top;
-#pragma unroll 4
-      for (int c = 0; c < parts; ++c) top = fmaxf(top, p.part_lse[c * R + w.at]);
-      const float base = top == -INFINITY ? 0.f : top, f = sum > 0.f ? exp2f(own - base) / sum : 0.f;
-      a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
-      float weight = exp2f(own - base);
-#pragma unroll 4
-      for (int c = 0; c < parts; ++c) {
-        const float g = exp2f(p.part_lse[c * R + w.at] - base);
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (c * R + w.at) * DH + d);
-        weight += g;
-        a.x += g * v.x;
-        a.y += g * v.y;
-        a.z += g * v.z;
-        a.w += g * v.w;
-      }
-      sum = weight;
-      ms = base;
+    const float* src = p.part_o + w.at * DH + d;
+#pragma unroll 8
+    for (int c = 0; c < parts; ++c) {
+      const float f = weights(r)[c];
+      const float4 v = *reinterpret_cast<const float4*>(src + c * R * DH);
+      sum += f;
+      a.x += f * v.x;
+      a.y += f * v.y;
+      a.z += f * v.z;
+      a.w += f * v.w;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
@@ -352,7 +374,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 constexpr int kWideFrom = 48;
 
 struct PrefixPlan {
-  int p_wide, s_wide;          // row tiles (1 or 2) of the wide kernel's CTAs, 0: the thin kernel takes the part
+  bool p_wide, s_wide;         // whether the wide kernel takes the part (else the thin one)
   bool merge;                  // own parts add the prefix's partial results
   long long p_tiles, s_tiles;  // row tiles: of all groups (a bound), of an entry
   long long rows;
@@ -395,18 +417,17 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
   PrefixPlan r{};
   r.rows = static_cast<long long>(B) * T * Hq;
   const bool fits = G <= kWideTile;  // (a token's heads stay in one row tile)
-  if (fits && NG > 0 && B * tg >= static_cast<long long>(kWideFrom) * NG)
-    r.p_wide = B * tg > static_cast<long long>(wide_rows(G)) * NG ? 2 : 1;
-  if (fits && tg >= kWideFrom) r.s_wide = tg > wide_rows(G) ? 2 : 1;
-  const int p_rows = r.p_wide ? r.p_wide * wide_rows(G) : kThinRows;
-  const int s_rows = r.s_wide ? r.s_wide * wide_rows(G) : kThinRows;
+  r.p_wide = fits && NG > 0 && B * tg >= static_cast<long long>(kWideFrom) * NG;
+  r.s_wide = fits && tg >= kWideFrom;
+  const int p_rows = r.p_wide ? wide_rows(G) : kThinRows;
+  const int s_rows = r.s_wide ? wide_rows(G) : kThinRows;
   r.p_tiles = NG > 0 ? (B * tg + static_cast<long long>(NG) * (p_rows - 1)) / p_rows : 0;
   r.s_tiles = (tg + s_rows - 1) / s_rows;
   const int sms = plan_sms(), thin_slots = sms * (kv.head_dim == 64 ? 4 : 2);
   const long long p_items = r.p_tiles * kv.n_kv_heads, s_items = B * r.s_tiles * kv.n_kv_heads;
-  const auto chunks = [&](int wide, long long items, int tokens, int join) {
-    return wide ? plan_chunks(items, tokens, sms * (3 - wide), kMinChunkPages, 3, join, 64)
-                : plan_chunks(items, tokens, thin_slots, kMinChunkPages, 2, join, 128);
+  const auto chunks = [&](bool wide, long long items, int tokens, int join) {
+    return wide ? plan_chunks(items, tokens, 2 * sms, kMinChunkPages, 3, join, kMaxParts / 2)
+                : plan_chunks(items, tokens, thin_slots, kMinChunkPages, 2, join, kMaxParts);
   };
   r.p_chunks = NG == 0 ? 0 : chunks(r.p_wide, p_items, mp, 0);
   r.s_chunks = chunks(r.s_wide, s_items, ml, 3);
@@ -477,10 +498,10 @@ cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int ele
   const long long n_prefix = plan.p_tiles * plan.p_chunks * p.Hkv, n_own = p.B * plan.s_tiles * plan.s_chunks * p.Hkv;
   cudaError_t e = cudaSuccess;
   if (n_prefix > 0)
-    e = plan.p_wide ? launch_prefix_wide(p, elem, DH, plan.p_wide, n_prefix, 0, false, tq, tk, tv, s)
+    e = plan.p_wide ? launch_prefix_wide(p, elem, DH, n_prefix, 0, false, tq, tk, tv, s)
                     : launch_thin<T16, DH>(p, n_prefix, 0, false, tk, tv, s);
   if (e == cudaSuccess)
-    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, plan.s_wide, 0, n_own, n_prefix > 0, tq, tk, tv, s)
+    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, 0, n_own, n_prefix > 0, tq, tk, tv, s)
                     : launch_thin<T16, DH>(p, 0, n_own, n_prefix > 0, tk, tv, s);
   if (e != cudaSuccess || p.merge || (p.NG == 0 && p.s_chunks == 1)) return e;
   // few rows of many parts: a row's parts over all the warps of a CTA

@@ -247,12 +247,12 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// prefix_wide.cu: items of one or two tiles of wide_rows(G) query rows (whole
-// tokens), n_prefix prefix items or n_own own ones.
+// prefix_wide.cu: items of a tile of wide_rows(G) query rows (whole tokens),
+// n_prefix prefix items or n_own own ones.
 constexpr int kWideTile = 128;  // rows of an MMA
 __host__ __device__ inline int wide_rows(int G) { return kWideTile / G * G; }
-cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, int tiles, long long n_prefix,
-                               long long n_own, bool behind, const CUtensorMap& tq, const CUtensorMap& tk,
-                               const CUtensorMap& tv, cudaStream_t s);
+cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, long long n_prefix, long long n_own,
+                               bool behind, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t s);
 
 }  // namespace dflash

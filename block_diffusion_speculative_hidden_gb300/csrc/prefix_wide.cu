@@ -1,15 +1,15 @@
 // Prefix attention, items of many query rows: the fifth-generation tensor
-// cores (tcgen05) with one or two tiles of 128 query rows a CTA.
+// cores (tcgen05) with a tile of 128 query rows a CTA and two CTAs an SM.
 //
-// Per tile of 128 keys and row tile: S = Q K^T into TMEM (one MMA chain, Q and
-// K from shared memory), P = 2^(S scale - m) rounded to 16 bits over S's own
-// columns, and O += P V with P as the A operand from TMEM.  Eight warps a row
-// tile run the softmax, two threads a query row (its TMEM lane), each with
-// half of the keys and of the head's dimensions.  Two row tiles share the K / V
-// stream and alternate on the tensor pipe: while one tile's softmax runs, the
-// other tile's products do.  m is the maximum of a row's first tile and moves
-// (O is then rescaled in TMEM) only when a later tile's P sums to 2^14 or
-// more, so P stays within 16 bits and most tiles need no maximum.
+// Per tile of 128 keys: S = Q K^T into TMEM (one MMA chain, Q and K from shared
+// memory), P = 2^(S scale - m) rounded to 16 bits into TMEM, and O += P V with
+// P as the A operand from there.  Eight warps run the softmax, two threads a
+// query row (its TMEM lane), each with half of the keys and of the head's
+// dimensions.  While one CTA's softmax runs, the other's products do; with 64
+// dimensions S(j + 1) is made under the softmax of tile j as well.  m is the
+// maximum of a row's first tile and moves (O is then rescaled in TMEM) only
+// when a later tile's P sums to 2^14 or more, so P stays within 16 bits and
+// most tiles need no maximum.
 #include "prefix_common.cuh"
 
 namespace dflash {
@@ -20,38 +20,37 @@ constexpr int kWideKeys = 128;       // keys of a tile
 constexpr int kWidePages = kWideKeys / kPage;
 constexpr int kWideLazy = 14;        // how far (in powers of two) a tile's P may sum up before m moves
 
-// NT row tiles.  Two take all of an SM (TMEM: two S and two O); with one, two
-// CTAs share an SM, so that one's start and end run beside the other's middle.
-template <int DH, int NT>
+template <int DH>
 struct WideLayout {
-  static constexpr int SOFT = 8 * NT;                       // softmax warps; then the TMA warp, the MMA warp and
+  static constexpr int SOFT = 8;                            // softmax warps; then the TMA warp, the MMA warp and
   static constexpr int THREADS = (SOFT + 4) * 32;           // two warps that only hand their registers on
   // registers a thread: at launch, and after the warps' exchange
-  static constexpr int REGS = NT == 2 ? 96 : 80;
-  static constexpr int SOFT_REGS = NT == 2 ? 112 : 104, FEED_REGS = 32;
+  static constexpr int REGS = 80, SOFT_REGS = 104, FEED_REGS = 32;
   static_assert(SOFT * SOFT_REGS + 4 * FEED_REGS <= (SOFT + 4) * REGS, "the exchange stays within the launch's registers");
   static constexpr int NCH = DH / 64;                       // 128-byte column chunks of a head
   static constexpr int Q_CH = kWideTile * 128;
-  static constexpr int Q_TILE = NCH * Q_CH;
+  static constexpr int Q_BYTES = NCH * Q_CH;
   static constexpr int KV_CH = kWideKeys * 128;
   static constexpr int SLOT = NCH * KV_CH;                  // a K or a V tile
-  static constexpr int NS = DH == 128 ? (NT == 2 ? 4 : 2) : (NT == 2 ? 8 : 5);  // ring slots: K(0), V(0), K(1), ..
-  static constexpr int OFF_KV = NT * Q_TILE;
+  static constexpr int NS = DH == 128 ? 2 : 5;              // ring slots: K(0), V(0), K(1), ..
+  static constexpr int OFF_KV = Q_BYTES;
   static constexpr int OFF_RED = OFF_KV + NS * SLOT;        // [2][warp][lane] row maxima, sums
   static constexpr int OFF_BAR = OFF_RED + 2 * SOFT * 32 * 4;
   static constexpr int SMEM = 1024 + OFF_BAR + 256;
-  static constexpr uint32_t S_COL = 0, O_COL = NT * kWideKeys;  // TMEM: S (and P) of every row tile, then O
-  static constexpr uint32_t COLS = NT * 256;
-  static_assert(O_COL + NT * DH <= COLS, "the accumulators fit TMEM");
-  static_assert(SMEM <= (NT == 2 ? 232448 : 115712), "shared memory of a CTA");
-  static_assert((2 * NS + 5 * NT) * 8 + 8 <= 256, "barriers fit their area");
+  // TMEM: S, then O; with 128 dimensions P lies over S (each page's 16 keys in
+  // the first 8 of its own 16 columns), with 64 there is room for it beside
+  static constexpr bool P_APART = DH == 64;
+  static constexpr uint32_t S_COL = 0, P_COL = P_APART ? kWideKeys : 0, O_COL = P_APART ? kWideKeys * 3 / 2 : kWideKeys;
+  static constexpr uint32_t P_PAGE = P_APART ? 8 : 16, COLS = 256;
+  static_assert(O_COL + DH <= COLS, "the accumulators fit TMEM");
+  static_assert(SMEM <= 115712, "shared memory of a CTA");
+  static_assert((2 * NS + 6) * 8 + 8 <= 256, "barriers fit their area");
   // the CTAs that an SM can hold by their shared memory find room in its 512
   // TMEM columns: an allocation never waits for another CTA's
   static_assert((512 / COLS + 1) * (SMEM + 1024) > 233472, "no more CTAs an SM than TMEM has room for");
   // at the end Q and the ring stage the output rows (fp32, or 16 bits)
   static constexpr int PITCH = DH * 4 + 16;
-  static constexpr int STAGE = kWideTile * PITCH;
-  static_assert(NT * STAGE <= OFF_RED, "the staged rows fit");
+  static_assert(kWideTile * PITCH <= OFF_RED, "the staged rows fit");
 };
 
 template <int N>
@@ -112,23 +111,24 @@ __device__ __forceinline__ constexpr uint32_t wide_idesc(int m, int n, bool b_mn
   return mma_idesc_f16_f32(m, n, b_mn) | (std::is_same<T16, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u);
 }
 
-template <typename T16, int DH, int NT>
-__global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
+template <typename T16, int DH>
+__global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     k_prefix_wide(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p, int n_prefix) {
-  using L = WideLayout<DH, NT>;
+  using L = WideLayout<DH>;
   using M16 = Mma16<T16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(smem + L::OFF_RED);
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* kv_empty = kv_full + L::NS;
-  uint64_t* q_full = kv_empty + L::NS;  // [NT]: per row tile, like the next four
-  uint64_t* s_full = q_full + NT;
-  uint64_t* p_full = s_full + NT;
-  uint64_t* o_full = p_full + NT;
-  uint64_t* part_full = o_full + NT;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_full + NT);
+  uint64_t* q_full = kv_empty + L::NS;
+  uint64_t* s_full = q_full + 1;
+  uint64_t* s_read = s_full + 1;  // S is in registers (P_APART)
+  uint64_t* p_full = s_read + 1;
+  uint64_t* o_full = p_full + 1;
+  uint64_t* part_full = o_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_full + 1);
   // (through a shuffle, so that what follows from it is known to be alike in a warp)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr int kTmaWarp = L::SOFT, kMmaWarp = L::SOFT + 1;
@@ -136,23 +136,21 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
   pdl_trigger();  // (the kernels behind wait for this one's results on their own)
   const int rows_tile = wide_rows(p.G);
   Item it;
-  if (!find_item(p, blockIdx.x, n_prefix, NT * rows_tile, it)) return pdl_wait();
+  if (!find_item(p, blockIdx.x, n_prefix, rows_tile, it)) return pdl_wait();
   const int np = max(0, it.pg1 - it.pg0);
-  const int n = (np + kWidePages - 1) / kWidePages;                    // key tiles
-  const int nt = NT == 2 && it.rows - it.row0 > rows_tile ? 2 : 1;     // row tiles
+  const int n = (np + kWidePages - 1) / kWidePages;  // key tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::NS; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
-    for (int t = 0; t < NT; ++t) {
-      mbar_init(&q_full[t], 1);
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 256);
-      mbar_init(&o_full[t], 1);
-      mbar_init(&part_full[t], kWideTile);
-    }
+    mbar_init(q_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_read, 256);
+    mbar_init(p_full, 256);
+    mbar_init(o_full, 1);
+    mbar_init(part_full, kWideTile);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -187,13 +185,9 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
       bool ok = true;
       if (lane == 0 && n > 0) {
         // whole tokens: a tile's first row is a token's first head of the group
-        const int token = it.b0 * p.T + it.row0 / p.G, tokens = kWideTile / p.G;
-        for (int t = 0; t < nt; ++t) {
-          mbar_arrive_expect_tx(&q_full[t], rows_tile * L::NCH * 128);
-          for (int cc = 0; cc < L::NCH; ++cc)
-            tma_rows(smem_u32(smem + t * L::Q_TILE + cc * L::Q_CH), &tmQ, &q_full[t], cc * 64, it.kvh * p.G,
-                     token + t * tokens);
-        }
+        mbar_arrive_expect_tx(q_full, rows_tile * L::NCH * 128);
+        for (int cc = 0; cc < L::NCH; ++cc)
+          tma_rows(smem_u32(smem + cc * L::Q_CH), &tmQ, q_full, cc * 64, it.kvh * p.G, it.b0 * p.T + it.row0 / p.G);
       }
       for (int j = 0; ok && j < n; ++j) {
         const int id = next, npb = min(kWidePages, np - j * kWidePages);
@@ -214,37 +208,39 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
         }
       }
       // every copy has landed before the CTA may leave
-      if (lane == 0 && n > 0)
-        for (int t = 0; t < nt; ++t) mbar_wait(&q_full[t], 0, p.status);
+      if (lane == 0 && n > 0) mbar_wait(q_full, 0, p.status);
       for (int i = max(0, issued - L::NS); i < issued; ++i) mbar_wait(&kv_full[i % L::NS], (i / L::NS) & 1, p.status);
     } else if (warp == kMmaWarp) {
-      // ---------------- MMAs.  S(j + 1) of a row tile overwrites its P(j), so
-      // it waits for P(j) V; the other row tile's products fill that time.  The
-      // whole warp walks along and one thread issues: the operands are then
-      // uniform values (computed by that thread alone, each of them crosses
-      // over to the uniform registers on its own, 110 cycles an MMA of 64).
+      // ---------------- MMAs.  Where P lies over S, S(j + 1) waits for P(j) V,
+      // else only for the softmax to have S(j) in registers.  The whole warp
+      // walks along and one thread issues: the operands are then uniform values
+      // (computed by that thread alone, each of them crosses over to the uniform
+      // registers on its own: 110 cycles an MMA of 64).
       const int key_tiles = __shfl_sync(0xffffffffu, n, 0), pages = __shfl_sync(0xffffffffu, np, 0);
-      const int row_tiles = __shfl_sync(0xffffffffu, nt, 0);
       const bool elected = elect_one();
       const uint64_t qd = sw128_desc(smem_u32(smem), 16, 1024), kd = sw128_desc(smem_u32(smem + L::OFF_KV), 16, 1024);
       const uint64_t vd = sw128_desc(smem_u32(smem + L::OFF_KV), L::KV_CH, 1024);
-      auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
-      auto kv_wait = [&](int i) { return all(mbar_wait_spin(&kv_full[i % L::NS], (i / L::NS) & 1, p.status)); };
+      auto wait = [&](uint64_t* bar, int phase) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_spin(bar, phase & 1, p.status)) != 0;
+        tc_fence_after();
+        return ok;
+      };
+      auto kv_wait = [&](int i) { return wait(&kv_full[i % L::NS], i / L::NS); };
       // (a descriptor's address field counts 16 bytes)
-      auto issue_s = [&](int t, int j) {
-        const uint64_t a = qd + t * (L::Q_TILE >> 4), k = kd + (2 * j) % L::NS * (L::SLOT >> 4);
+      auto issue_s = [&](int j) {
+        const uint64_t k = kd + (2 * j) % L::NS * (L::SLOT >> 4);
         const uint32_t id = wide_idesc<T16>(kWideTile, 16 * min(kWidePages, pages - j * kWidePages), false);
         if (elected) {
 #pragma unroll
           for (int ks = 0; ks < DH / 16; ++ks)
-            tc_mma_bf16(tmem + L::S_COL + t * kWideKeys, a + ((ks >> 2) * L::Q_CH + (ks & 3) * 32 >> 4),
-                        k + ((ks >> 2) * L::KV_CH + (ks & 3) * 32 >> 4), id, ks > 0 ? 1u : 0u);
-          tc_commit(&s_full[t]);
-          if (t == row_tiles - 1) tc_commit(&kv_empty[(2 * j) % L::NS]);
+            tc_mma_bf16(tmem + L::S_COL, qd + (((ks >> 2) * L::Q_CH + (ks & 3) * 32) >> 4),
+                        k + (((ks >> 2) * L::KV_CH + (ks & 3) * 32) >> 4), id, ks > 0 ? 1u : 0u);
+          tc_commit(s_full);
+          tc_commit(&kv_empty[(2 * j) % L::NS]);
         }
         __syncwarp();
       };
-      auto issue_o = [&](int t, int j) {
+      auto issue_o = [&](int j) {
         const uint64_t v = vd + (2 * j + 1) % L::NS * (L::SLOT >> 4);
         const int npb = min(kWidePages, pages - j * kWidePages);
         const uint32_t id = wide_idesc<T16>(kWideTile, DH, true);
@@ -252,45 +248,39 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
 #pragma unroll
           for (int ks = 0; ks < kWidePages; ++ks)
             if (ks < npb)
-              tc_mma_bf16_ts(tmem + L::O_COL + t * DH, tmem + L::S_COL + t * kWideKeys + 16 * ks, v + ks * (2048 >> 4), id,
+              tc_mma_bf16_ts(tmem + L::O_COL, tmem + L::P_COL + L::P_PAGE * ks, v + ks * (2048 >> 4), id,
                              (j | ks) > 0 ? 1u : 0u);
-          tc_commit(&o_full[t]);
-          if (t == row_tiles - 1) tc_commit(&kv_empty[(2 * j + 1) % L::NS]);
+          tc_commit(o_full);
+          tc_commit(&kv_empty[(2 * j + 1) % L::NS]);
         }
         __syncwarp();
       };
-      bool ok = key_tiles > 0 && kv_wait(0);
-      for (int t = 0; ok && t < row_tiles; ++t) {
-        ok = all(mbar_wait_spin(&q_full[t], 0, p.status));
-        tc_fence_after();
-        if (ok) issue_s(t, 0);
-      }
+      bool ok = key_tiles > 0 && wait(q_full, 0) && kv_wait(0);
+      if (ok) issue_s(0);
       for (int j = 0; ok && j < key_tiles; ++j) {
-        ok = kv_wait(2 * j + 1);
-        for (int t = 0; ok && t < row_tiles; ++t) {
-          ok = all(mbar_wait_spin(&p_full[t], j & 1, p.status));
-          tc_fence_after();
-          if (!ok) break;
-          issue_o(t, j);
-          if (j + 1 < key_tiles) {
-            ok = (t > 0 || kv_wait(2 * j + 2)) && all(mbar_wait_spin(&o_full[t], j & 1, p.status));
-            tc_fence_after();
-            if (ok) issue_s(t, j + 1);
-          }
+        if (L::P_APART && j + 1 < key_tiles) {
+          ok = kv_wait(2 * j + 2) && wait(s_read, j);
+          if (ok) issue_s(j + 1);
+        }
+        ok = ok && kv_wait(2 * j + 1) && wait(p_full, j);
+        if (ok) issue_o(j);
+        if (!L::P_APART && j + 1 < key_tiles) {
+          ok = ok && kv_wait(2 * j + 2) && wait(o_full, j);
+          if (ok) issue_s(j + 1);
         }
       }
     }
-  } else if (warp < 8 * nt) {
+  } else {
     regs_up<L::SOFT_REGS>();
-    // ---------------- softmax: threads r of the two halves of row tile t own row r
-    const int t = warp >> 3, quad = warp & 3, half = warp >> 2 & 1, r = quad * 32 + lane;
-    const int pair = 1 + t * 4 + quad;  // the named barrier of the row's two warps
-    Row row = find_row(p, it, it.row0 + t * rows_tile + r);
+    // ---------------- softmax: threads r of the two halves own row r
+    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
+    const int pair = 1 + quad;  // the named barrier of the row's two warps
+    Row row = find_row(p, it, it.row0 + r);
     row.live = row.live && r < rows_tile;
     const int parts = it.last && p.merge ? prefix_parts(p, it.b0) : 0;  // of the prefix, to be added at the end
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t s_at = tmem + lanes + L::S_COL + t * kWideKeys + 64 * half;
-    const uint32_t o_at = tmem + lanes + L::O_COL + t * DH + DH / 2 * half;
+    const uint32_t s_at = tmem + lanes + L::S_COL + 64 * half, p_at = tmem + lanes + L::P_COL + 4 * L::P_PAGE * half;
+    const uint32_t o_at = tmem + lanes + L::O_COL + DH / 2 * half;
     auto partner = [&](int slot, float v) {  // the other half's value
       red[(slot * L::SOFT + warp) * 32 + lane] = v;
       wide_bar(pair, 64);
@@ -301,7 +291,7 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
     for (int j = 0; j < n; ++j) {
       const int npb = min(kWidePages, np - j * kWidePages);
       const int key0 = (it.pg0 + j * kWidePages) * kPage;
-      ok = ok && mbar_wait(&s_full[t], j & 1, p.status);
+      ok = ok && mbar_wait(s_full, j & 1, p.status);
       __syncwarp();
       tc_fence_after();
       uint32_t sv[4][16];
@@ -309,6 +299,14 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
       for (int g = 0; g < 4; ++g)
         if (4 * half + g < npb) tc_ld_32x32b_x16_nw(s_at + 16 * g, sv[g]);
       tc_wait_ld();
+      if (L::P_APART) {
+        tc_fence_before();
+        mbarrier_arrive_one(s_read);
+        // (P(j - 1) V is done before its P is written over, and O is then at rest)
+        if (j > 0) ok = ok && mbar_wait(o_full, (j - 1) & 1, p.status);
+        __syncwarp();
+        tc_fence_after();
+      }
       // keys of this half that the row sees (the chunk may end inside the tile)
       const int lim = min(row.seen, it.pg1 * kPage) - key0 - 64 * half;
       if (__any_sync(0xffffffffu, lim < 64)) {
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
               mx[e] = wide_max3(mx[e], __uint_as_float(sv[g][k + 2 * e]), __uint_as_float(sv[g][k + 2 * e + 1]));
         return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       };
-      // P against m, over the first half of each page's own columns; returns its sum
+      // P against m; returns its sum
       auto make_p = [&]() {
         const float mu = m == -INFINITY ? 0.f : m;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), mneg2 = make_float2(-mu, -mu);
@@ -345,7 +343,7 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
             sum[k & 1] = __fadd2_rn(sum[k & 1], e);
             pk[k] = M16::pack(e.x, e.y);
           }
-          tc_st_32x32b_x8(s_at + 16 * g, pk);
+          tc_st_32x32b_x8(p_at + L::P_PAGE * g, pk);
         }
         return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       };
@@ -368,7 +366,7 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
           const float cand = fmaxf(m, top * p.scale_log2);
           const float al = cand > m ? wide_ex2(m - cand) : 1.f;  // (m = -infinity: 0)
           m = cand;
-          // S(j) was issued after P(j - 1) V was done, so O is at rest
+          // (where P lies over S, S(j) was issued after P(j - 1) V was done)
 #pragma unroll
           for (int d = 0; d < DH / 2; d += 16) {
             uint32_t v[16];
@@ -396,11 +394,10 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
       }
       tc_wait_st();
       tc_fence_before();
-      mbarrier_arrive_one(&p_full[t]);
+      mbarrier_arrive_one(p_full);
     }
-    // the last product of every row tile: then O is whole, and Q and the ring are free
-    if (n > 0)
-      for (int q = 0; q < nt; ++q) ok = ok && mbar_wait(&o_full[q], (n - 1) & 1, p.status);
+    // the last product: then O is whole, and Q and the ring are free
+    if (n > 0) ok = ok && mbar_wait(o_full, (n - 1) & 1, p.status);
     __syncwarp();
     tc_fence_after();
     l += partner(n & 1, l);
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
       }
     }
     const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-    uint8_t* stage = smem + t * L::STAGE + r * L::PITCH;
+    uint8_t* stage = smem + r * L::PITCH;
     if (it.last && parts > 0) {
       // add the prefix's partial results, a copy of the row at a time (in order)
       pdl_wait();
@@ -428,16 +425,16 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
       for (int c = 0; c < parts; ++c) {
         if (half == 0) {
           if (row.live) {
-            mbar_arrive_expect_tx(&part_full[t], DH * 4);
-            bulk_load_global(smem_u32(stage), p.part_o + (c * R + row.at) * DH, DH * 4, &part_full[t]);
+            mbar_arrive_expect_tx(part_full, DH * 4);
+            bulk_load_global(smem_u32(stage), p.part_o + (c * R + row.at) * DH, DH * 4, part_full);
           } else {
-            mbarrier_arrive_one(&part_full[t]);
+            mbarrier_arrive_one(part_full);
           }
         }
         const float other = row.live ? p.part_lse[c * R + row.at] : -INFINITY;
         const float top = fmaxf(lse2, other), base = top == -INFINITY ? 0.f : top;
         const float f0 = wide_ex2(lse2 - base), f1 = wide_ex2(other - base);
-        ok = ok && mbar_wait(&part_full[t], c & 1, p.status);
+        ok = ok && mbar_wait(part_full, c & 1, p.status);
 #pragma unroll
         for (int d = 0; d < DH / 2; d += 4) {
           const float4 y = *reinterpret_cast<const float4*>(stage + (DH / 2 * half + d) * 4);
@@ -492,36 +489,29 @@ __global__ void __launch_bounds__(WideLayout<DH, NT>::THREADS, 3 - NT)
   pdl_wait();  // (the joining kernel behind starts once all of this one has left)
 }
 
-template <typename T16, int DH, int NT>
+template <typename T16, int DH>
 cudaError_t launch_wide_t(const PrefixParams& p, long long n_prefix, long long n_own, bool behind,
                           const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  using L = WideLayout<DH, NT>;
+  using L = WideLayout<DH>;
   static FuncAttr attr;
   const cudaError_t e = attr.ensure(L::SMEM, [](int v) {
-    return cudaFuncSetAttribute(k_prefix_wide<T16, DH, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+    return cudaFuncSetAttribute(k_prefix_wide<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
   });
   if (e != cudaSuccess) return e;
-  return launch_k(k_prefix_wide<T16, DH, NT>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(L::THREADS), L::SMEM,
-                  s, dim3(1), behind, tq, tk, tv, p, static_cast<int>(n_prefix));
-}
-
-template <typename T16, int DH>
-cudaError_t launch_wide_n(const PrefixParams& p, int tiles, long long n_prefix, long long n_own, bool behind,
-                          const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  return tiles == 2 ? launch_wide_t<T16, DH, 2>(p, n_prefix, n_own, behind, tq, tk, tv, s)
-                    : launch_wide_t<T16, DH, 1>(p, n_prefix, n_own, behind, tq, tk, tv, s);
+  return launch_k(k_prefix_wide<T16, DH>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(L::THREADS), L::SMEM, s,
+                  dim3(1), behind, tq, tk, tv, p, static_cast<int>(n_prefix));
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, int tiles, long long n_prefix,
-                               long long n_own, bool behind, const CUtensorMap& tq, const CUtensorMap& tk,
-                               const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, long long n_prefix, long long n_own,
+                               bool behind, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t s) {
   if (elem == DFLASH_ELEM_BF16)
-    return head_dim == 64 ? launch_wide_n<__nv_bfloat16, 64>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s)
-                          : launch_wide_n<__nv_bfloat16, 128>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s);
-  return head_dim == 64 ? launch_wide_n<__half, 64>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s)
-                        : launch_wide_n<__half, 128>(p, tiles, n_prefix, n_own, behind, tq, tk, tv, s);
+    return head_dim == 64 ? launch_wide_t<__nv_bfloat16, 64>(p, n_prefix, n_own, behind, tq, tk, tv, s)
+                          : launch_wide_t<__nv_bfloat16, 128>(p, n_prefix, n_own, behind, tq, tk, tv, s);
+  return head_dim == 64 ? launch_wide_t<__half, 64>(p, n_prefix, n_own, behind, tq, tk, tv, s)
+                        : launch_wide_t<__half, 128>(p, n_prefix, n_own, behind, tq, tk, tv, s);
 }
 
 }  // namespace dflash
