@@ -34,331 +34,492 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 
 constexpr int kThinWarps = 4;
 constexpr int kThinThreads = kThinWarps * 32;
-constexpr int kThinRows = 16;   // query rows of a tile (one MMA's rows)
 constexpr int kThinStages = 3;  // pages in flight per warp
-constexpr int kMaxParts = 128;  // chunks of a prefix
+constexpr int kThinPages = 2;   // pages that a warp takes at least
+constexpr int kMaxEntries = 4096;  // batch entries, and groups, of a call
 
 template <int DH>
 struct ThinLayout {
   static constexpr int HALF_PAGE = kPage * DH * 2;        // bytes of a page of K (or V) of one head
   static constexpr int STAGE = 2 * HALF_PAGE;
   static constexpr int WARP = kThinStages * STAGE;
-  static constexpr int LDO = DH + 8;                      // floats per row of a warp's partial output
-  static constexpr int OFF_ML = kThinWarps * WARP;        // [warps][16][2] maxima and sums
-  static constexpr int OFF_TOP = OFF_ML + kThinWarps * kThinRows * 8;  // [16] what the weights are relative to
-  static constexpr int OFF_W = kThinRows * LDO * 4;       // weights of four rows' parts, in each warp's ring
-  static_assert(OFF_W + 4 * kMaxParts * 4 <= WARP, "the weights fit beside a warp's partial output");
-  static constexpr int OFF_BAR = OFF_TOP + kThinRows * 4;
+  static constexpr int OFF_SCAN = kThinWarps * WARP;
+  static constexpr int OFF_BAR = OFF_SCAN + 64;
   static constexpr int BYTES = OFF_BAR + kThinWarps * kThinStages * 8;
-  static constexpr int SMEM = 1024 + BYTES;
-  static_assert(kThinRows * LDO * 4 <= WARP, "a warp's partial output fits its ring");
+  static constexpr int SMEM = 1024 + BYTES;               // + the line: first pages of its elements, their rows and pages
+  static_assert(BYTES % 16 == 0, "the line is aligned");
 };
 
-// One CTA: a tile of 16 query rows of one kv head over a chunk of pages.
-// Every warp takes every fourth page with a ring of its own, keeps its own
-// running maximum, sum and output, and the CTA joins its warps at the end.
-template <typename T16, int DH>
+// The thin kernel's work is a line of pages: for every group (where it takes
+// the prefixes) and then every entry, its row tiles x kv heads x pages.  Warp
+// w of the grid takes pages [w * per, (w + 1) * per) of the line, whatever
+// parts they belong to, so that all warps stream alike however uneven the
+// lengths are.  A part (one tile and head) that one warp takes whole goes to
+// whole_*; of one that several share, each leaves its share in its own slot:
+// 2w if the share starts at the warp's first page, 2w + 1 otherwise.
+// Rows and pages of element e (groups, then entries) of the line.
+struct ThinPart {
+  bool shared;
+  int b0, rows, tokens, table_row;
+};
+constexpr int kThinHeld = 512;  // elements whose rows and pages the CTA holds in shared memory
+__device__ __forceinline__ ThinPart thin_read(const PrefixParams& p, int groups, int e) {
+  ThinPart t;
+  t.shared = e < groups;
+  if (t.shared) {
+    t.b0 = p.group_off[e];
+    t.rows = (p.group_off[e + 1] - t.b0) * p.T * p.G;
+    t.table_row = p.prefix_seq[e];
+  } else {
+    t.b0 = e - groups;
+    t.rows = entry_rows(p, t.b0) * p.G;
+    t.table_row = p.seq != nullptr ? p.seq[t.b0] : t.b0;
+  }
+  t.tokens = seq_tokens(p, t.table_row);
+  return t;
+}
+__device__ __forceinline__ int thin_tiles(int rows, int tile) { return (rows + tile - 1) / tile; }
+
+// Where an element's rows and pages are held, behind the line's first pages.
+__device__ __forceinline__ int4* thin_held(long long* first, int n) {
+  return reinterpret_cast<int4*>(first + (n + 2) / 2 * 2);
+}
+
+// The same, from the copy that thin_line() left there.
+__device__ __forceinline__ ThinPart thin_part(const PrefixParams& p, int groups, long long* first, int e) {
+  const int n = groups + p.B;
+  if (n > kThinHeld) return thin_read(p, groups, e);
+  const int4 v = thin_held(first, n)[e];
+  return ThinPart{e < groups, v.x, v.y, v.z, v.w};
+}
+
+// Sets the line up: first[e] for every element and the length after the last
+// (the whole CTA of WARPS warps; ok: the group bounds are sound; check: look at
+// the elements' sequences and flag bad ones).
+template <int WARPS>
+__device__ __forceinline__ void thin_line(const PrefixParams& p, int groups, bool ok, bool check, long long* first,
+                                          int4* held, long long* scan) {
+  const int n = groups + p.B, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long before = 0;
+  for (int e0 = 0; e0 < n; e0 += WARPS * 32) {
+    const int e = e0 + threadIdx.x;
+    long long size = 0;
+    if (e < n && (e >= groups || ok)) {
+      const ThinPart t = thin_read(p, groups, e);
+      if (held != nullptr) held[e] = make_int4(t.b0, t.rows, t.tokens, t.table_row);
+      size = static_cast<long long>(thin_tiles(t.rows, p.thin_rows)) * p.Hkv * pages_of(t.tokens);
+      if (check) {
+        if (t.shared) check_prefix(p, t.table_row);
+        else check_entry(p, t.b0, t.table_row);
+      }
+    }
+    long long sum = size;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) scan[warp] = sum;
+    __syncthreads();
+    long long all = 0;
+    for (int q = 0; q < WARPS; ++q) {
+      if (q < warp) sum += scan[q];
+      all += scan[q];
+    }
+    if (e < n) first[e] = before + sum - size;
+    before += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) first[n] = before;
+  __syncthreads();
+}
+
+// The element that page f of the line belongs to: the last e with first[e] <= f.
+__device__ __forceinline__ int thin_find(const long long* first, int n, long long f) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= f) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// a / b of non-negative numbers (64-bit divisions are long; few need one).
+__device__ __forceinline__ long long thin_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+__device__ __forceinline__ long long thin_per(long long length, int warps) {
+  const long long per = thin_div(length + warps - 1, warps);
+  return per < kThinPages ? kThinPages : per;
+}
+
+__device__ __forceinline__ float thin_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The transpose of an 8 x 8 matrix of 16-bit values (row g, columns 2t and 2t + 1 in lane 4g + t).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+// Independent warps, each with a ring of pages that runs on over the parts it
+// takes, and its own running maxima, sums and outputs.  The products are taken
+// transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and dimensions fill
+// the 16 rows of an MMA and the few query rows its 8 columns (NR of them).
+template <typename T16, int DH, int NR>
 __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
-                                                              const __grid_constant__ PrefixParams p, int n_prefix) {
+                                                              const __grid_constant__ PrefixParams p) {
   using L = ThinLayout<DH>;
   using M = Mma16<T16>;
-  constexpr int KS = DH / 16, NT = DH / 8;
+  constexpr int KS = DH / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long* first = reinterpret_cast<long long*>(smem + L::BYTES);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int gr = lane >> 2, t4 = lane & 3;
 
-  Item it;
-  // (the kernel before it, where there is one, is waited for on every way
-  // out: the joining kernel behind starts once all of this one has left)
-  if (!find_item(p, blockIdx.x, n_prefix, kThinRows, it)) return pdl_wait();
-  const int pg0 = it.pg0, pg1 = it.pg1, tokens = it.tokens, kvh = it.kvh;
-  const Row row[2] = {find_row(p, it, it.row0 + gr), find_row(p, it, it.row0 + gr + 8)};
-
-  const int parts = it.last && p.merge ? prefix_parts(p, it.b0) : 0;  // of the prefix, to be added at the end
-
+  pdl_trigger();  // (the joining kernel waits for this one's results on its own)
+  const int groups = p.p_thin ? p.NG : 0, n_line = groups + p.B;
+  const bool sound = p.NG == 0 || bounds_ok(p);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !sound) flag_status(p.status, ST_BAD_BLOCK);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * kThinStages;
-  uint8_t* ring = smem + warp * L::WARP;
-  const int mine = pg1 > pg0 + warp ? (pg1 - pg0 - warp + kThinWarps - 1) / kThinWarps : 0;
   if (lane == 0) {
     for (int s = 0; s < kThinStages; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  __syncwarp();
-  // page ids of this warp's next 32 pages, one per lane
-  int ids = 0;
+  thin_line<kThinWarps>(p, groups, sound, blockIdx.x == 0, first, n_line <= kThinHeld ? thin_held(first, n_line) : nullptr,
+                        reinterpret_cast<long long*>(smem + L::OFF_SCAN));
+  const long long length = first[n_line], per = thin_per(length, p.warps);
+  if (blockIdx.x == 0 && n_line > kThinHeld) {  // (a shorter line the joining kernel sets up itself)
+    for (int e = threadIdx.x; e <= n_line; e += kThinThreads) p.work[e] = first[e];
+  }
+  const int self = blockIdx.x * kThinWarps + warp;
+  const long long f0 = self * per, f1 = min(length, f0 + per);
+  const int mine = f1 > f0 ? static_cast<int>(f1 - f0) : 0;
+  uint8_t* ring = smem + warp * L::WARP;
+
+  // page id and kv head of this warp's next 32 pages, one per lane
+  int ids = 0, heads = 0;
   auto fetch_ids = [&](int i0) {
     const int i = i0 + lane;
-    int id = 0;
     if (i < mine) {
-      id = p.page_table[static_cast<long long>(it.table_row) * p.max_pages + pg0 + warp + i * kThinWarps];
-      if (id < 0 || id >= p.n_pages) {
+      const int e = thin_find(first, n_line, f0 + i);
+      const ThinPart t = thin_part(p, groups, first, e);
+      const int pages = pages_of(t.tokens);
+      const long long x = f0 + i - first[e];
+      const int unit = static_cast<int>(thin_div(x, pages)), pg = static_cast<int>(x - static_cast<long long>(unit) * pages);
+      heads = unit % p.Hkv;
+      ids = p.page_table[static_cast<long long>(t.table_row) * p.max_pages + pg];
+      if (ids < 0 || ids >= p.n_pages) {
         flag_status(p.status, ST_BAD_PAGE);
-        id = p.n_pages;  // outside the tensor map: reads as zeros
+        ids = p.n_pages;  // outside the tensor map: reads as zeros
       }
     }
-    ids = id;
   };
+  const bool elected = elect_one();
   auto issue = [&](int i) {
-    if ((i & 31) == 0) fetch_ids(i);
-    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-    if (lane == 0) {
-      const int s = i % kThinStages;
-      const uint32_t kd = smem_u32(ring + s * L::STAGE);
-      mbar_arrive_expect_tx(&bars[s], L::STAGE);
-#pragma unroll
-      for (int c = 0; c < DH / 64; ++c) {
-        tma_page(kd + c * 2048, &tmK, &bars[s], c * 64, kvh, id);
-        tma_page(kd + L::HALF_PAGE + c * 2048, &tmV, &bars[s], c * 64, kvh, id);
-      }
-    }
-  };
-  for (int i = 0; i < min(mine, kThinStages); ++i) issue(i);
-
-  // the query rows as A fragments
-  uint32_t qf[KS][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const T16* src = static_cast<const T16*>(p.q) + row[i].token * p.ld_q + (row[i].at - row[i].token * p.Hq) * DH + 2 * t4;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      qf[ks][i] = row[i].live ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
-      qf[ks][2 + i] = row[i].live ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
-    }
-  }
-
-  float o[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  // ldmatrix lane addresses within a [16 keys][128 bytes] swizzled box
-  const int lr = lane & 7, lm = lane >> 3;
-  const int k_key = (lm >> 1) * 8 + lr, k_unit = lm & 1;   // K: matrices (keys, d), (keys, d + 8), (keys + 8, ..)
-  const int v_key = (lm & 1) * 8 + lr, v_unit = lm >> 1;   // V, transposed: (keys, d), (keys + 8, d), (keys, d + 8), ..
-
-  bool ok = true;
-  for (int i = 0; i < mine; ++i) {
+    if (i > 0 && (i & 31) == 0) fetch_ids(i);
+    const int id = __shfl_sync(0xffffffffu, ids, i & 31), head = __shfl_sync(0xffffffffu, heads, i & 31);
     const int s = i % kThinStages;
-    ok = ok && mbar_wait(&bars[s], (i / kThinStages) & 1, p.status);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    const int key0 = (pg0 + warp + i * kThinWarps) * kPage;
-    const uint32_t kd = smem_u32(ring + s * L::STAGE), vd = kd + L::HALF_PAGE;
-    // values past the last token would meet probabilities of zero: they must be finite
-    if (key0 + kPage > tokens) {
-      const int first = tokens - key0;
-      for (int e = lane; e < (kPage - first) * (DH / 64) * 8; e += 32) {
-        const int c = e / ((kPage - first) * 8), f = e % ((kPage - first) * 8);
-        *reinterpret_cast<uint4*>(ring + s * L::STAGE + L::HALF_PAGE + c * 2048 + first * 128 + f * 16) =
-            make_uint4(0, 0, 0, 0);
-      }
-      __syncwarp();
-    }
-    float sc[2][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      uint32_t kb[4];
-      const int unit = (ks & 3) * 2 + k_unit;
-      ldsm_x4(kd + (ks >> 2) * 2048 + k_key * 128 + ((unit ^ (k_key & 7)) << 4), kb);
-      M::mma(sc[0], qf[ks], kb[0], kb[1]);
-      M::mma(sc[1], qf[ks], kb[2], kb[3]);
-    }
-    uint32_t pa[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key0 + (e >> 1) * 8 + 2 * t4 + (e & 1);
-        x[e] = key < row[h].seen ? sc[e >> 1][2 * h + (e & 1)] * p.scale_log2 : -INFINITY;
-      }
-      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[h], mx), ms = mn == -INFINITY ? 0.f : mn;
-      const float al = exp2f(m[h] - ms);
-      m[h] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = exp2f(x[e] - ms);
-        sum += x[e];
-      }
-      l[h] = l[h] * al + sum;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        o[j][2 * h] *= al;
-        o[j][2 * h + 1] *= al;
-      }
-      pa[h] = M::pack(x[0], x[1]);
-      pa[2 + h] = M::pack(x[2], x[3]);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; j += 2) {
-      uint32_t vb[4];
-      const int unit = (j & 7) + v_unit;
-      ldsm_x4_t(vd + (j >> 3) * 2048 + v_key * 128 + ((unit ^ (v_key & 7)) << 4), vb);
-      M::mma(o[j], pa, vb[0], vb[1]);
-      M::mma(o[j + 1], pa, vb[2], vb[3]);
+    const uint32_t kd = smem_u32(smem) + warp * L::WARP + s * L::STAGE;
+    if (elected) {
+      mbar_arrive_expect_tx(&bars[s], L::STAGE);
+      tma_page(kd, &tmK, &bars[s], 0, head, id);
+      tma_page(kd + L::HALF_PAGE, &tmV, &bars[s], 0, head, id);
     }
     __syncwarp();
-    if (i + kThinStages < mine) issue(i + kThinStages);
-  }
-  if (!ok) {  // a wait gave up: what is still in flight gets its own bounded waits before the CTA leaves
-    for (int s = 0; s < min(mine, kThinStages); ++s) mbar_wait(&bars[s], 0, p.status);
-  }
-
-  // join the warps: each leaves (m, l) and its unnormalised output in its ring
-  float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    const int r = gr + 8 * h;
-    if (t4 == 0) {
-      ml[(warp * kThinRows + r) * 2] = m[h];
-      ml[(warp * kThinRows + r) * 2 + 1] = l[h];
-    }
-    float* dst = reinterpret_cast<float*>(ring) + r * L::LDO + 2 * t4;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
-  }
-  __syncthreads();
+  };
+  // ldmatrix lane addresses within a [16 keys][128 bytes] swizzled box
+  const int lr = lane & 7, lm = lane >> 3;
+  const int k_key = (lm & 1) * 8 + lr, k_unit = lm >> 1;  // K: (keys, d), (keys + 8, d), (keys, d + 8), ..
+  const int v_key = (lm >> 1) * 8 + lr, v_unit = lm & 1;  // V, transposed: (keys, d), (keys, d + 8), (keys + 8, d), ..
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-  const int out_chunk = it.shared ? it.chunk : p.p_chunks + it.chunk;
-  // weights of the prefix's partial results (each is normalised by its own
-  // sum), eight threads a row, in the unused part of the rings
-  auto weights = [&](int r) { return reinterpret_cast<float*>(smem + r / 4 * L::WARP + L::OFF_W) + r % 4 * kMaxParts; };
-  if (parts > 0) {
-    pdl_wait();
-    const int r = threadIdx.x / 8;
-    const Row w = find_row(p, it, it.row0 + r);
-    float mx = -INFINITY;
+
+  fetch_ids(0);
+  bool ok = true;
+  int i = 0;
+  while (i < mine && ok) {
+    // the part that page i belongs to, and this warp's share of it
+    const int e = thin_find(first, n_line, f0 + i);
+    const ThinPart part = thin_part(p, groups, first, e);
+    const int pages = pages_of(part.tokens);
+    const long long x = f0 + i - first[e];
+    const int unit = static_cast<int>(thin_div(x, pages)), pg0 = static_cast<int>(x - static_cast<long long>(unit) * pages);
+    const int share = min(pages - pg0, mine - i);
+    Item it;
+    it.shared = part.shared;
+    it.b0 = part.b0;
+    it.rows = part.rows;
+    it.tokens = part.tokens;
+    it.kvh = unit % p.Hkv;
+    it.row0 = unit / p.Hkv * (8 * NR);
+
+    // query row 8j + gr as a B fragment
+    uint32_t qf[NR][KS][2];
 #pragma unroll
-    for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
-    float top = mx;
-    if (w.live)
-      for (int c = threadIdx.x % 8; c < parts; c += 8) {
-        const float v = p.part_lse[c * R + w.at];
-        weights(r)[c] = v;
-        top = fmaxf(top, v);
+    for (int j = 0; j < NR; ++j) {
+      const Row row = find_row(p, it, it.row0 + 8 * j + gr);
+      const T16* src = static_cast<const T16*>(p.q) + row.token * p.ld_q + (row.at - row.token * p.Hq) * DH + 2 * t4;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[j][ks][0] = row.live ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+        qf[j][ks][1] = row.live ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+      }
+    }
+    if (i == 0) {  // (the pages' first copies, behind the loads of the first queries)
+      for (int c = 0; c < min(mine, kThinStages); ++c) issue(c);
+    }
+    // rows 8j + 2 t4 and the next one are this thread's in S^T and O^T
+    int seen[NR][2];
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) seen[j][c] = find_row(p, it, it.row0 + 8 * j + 2 * t4 + c).seen;
+    float o[NR][KS][4] = {};
+    float m[NR][2], l[NR][2] = {};
+#pragma unroll
+    for (int j = 0; j < NR; ++j) m[j][0] = m[j][1] = -INFINITY;
+
+    for (int c = 0; c < share; ++c, ++i) {
+      const int s = i % kThinStages;
+      ok = ok && mbar_wait(&bars[s], (i / kThinStages) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      if (!ok) break;
+      const int key0 = (pg0 + c) * kPage;
+      const uint32_t kd = smem_u32(ring + s * L::STAGE), vd = kd + L::HALF_PAGE;
+      // values past the last token would meet probabilities of zero: they must be finite
+      if (key0 + kPage > it.tokens) {
+        const int held = it.tokens - key0;
+        for (int z = lane; z < (kPage - held) * (DH / 64) * 8; z += 32) {
+          const int ch = z / ((kPage - held) * 8), f = z % ((kPage - held) * 8);
+          *reinterpret_cast<uint4*>(ring + s * L::STAGE + L::HALF_PAGE + ch * 2048 + held * 128 + f * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // (a later page's copy comes to the same place)
+        __syncwarp();
+      }
+      float sc[NR][2][4] = {};  // (two chains: the products of even and odd steps)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t ka[4];
+        const int u = (ks & 3) * 2 + k_unit;
+        ldsm_x4(kd + (ks >> 2) * 2048 + k_key * 128 + ((u ^ (k_key & 7)) << 4), ka);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) M::mma(sc[j][ks & 1], ka, qf[j][ks][0], qf[j][ks][1]);
+      }
+      uint32_t pb[NR][2];
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        // z[q]: key gr + 8 (q / 2), row 8j + 2 t4 + q % 2
+        float z[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          z[q] = key0 + gr + (q >> 1) * 8 < seen[j][q & 1] ? (sc[j][0][q] + sc[j][1][q]) * p.scale_log2 : -INFINITY;
+        float al[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = fmaxf(z[h], z[2 + h]);
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const float mn = fmaxf(m[j][h], mx), ms = mn == -INFINITY ? 0.f : mn;
+          al[h] = thin_ex2(m[j][h] - ms);
+          m[j][h] = mn;
+          z[h] = thin_ex2(z[h] - ms);
+          z[2 + h] = thin_ex2(z[2 + h] - ms);
+          l[j][h] = l[j][h] * al[h] + (z[h] + z[2 + h]);
+        }
+        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+          for (int d = 0; d < KS; ++d)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[j][d][q] *= al[q & 1];
+        }
+        pb[j][0] = transpose8(M::pack(z[0], z[1]));
+        pb[j][1] = transpose8(M::pack(z[2], z[3]));
       }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.f : top;
-    if (w.live)
-      for (int c = threadIdx.x % 8; c < parts; c += 8) weights(r)[c] = exp2f(weights(r)[c] - base);
-    if (threadIdx.x % 8 == 0) reinterpret_cast<float*>(smem + L::OFF_TOP)[r] = base;
-    __syncthreads();
-  }
-  for (int e = threadIdx.x; e < kThinRows * (DH / 4); e += kThinThreads) {
-    const int r = e / (DH / 4), d = (e % (DH / 4)) * 4;
-    const Row w = find_row(p, it, it.row0 + r);
-    if (!w.live) continue;
-    float ms;
-    if (parts > 0) {
-      ms = reinterpret_cast<const float*>(smem + L::OFF_TOP)[r];
-    } else {
-      float mx = -INFINITY;
+      for (int d = 0; d < KS; ++d) {
+        uint32_t va[4];
+        const int u = (d & 3) * 2 + v_unit;
+        ldsm_x4_t(vd + (d >> 2) * 2048 + v_key * 128 + ((u ^ (v_key & 7)) << 4), va);
 #pragma unroll
-      for (int q = 0; q < kThinWarps; ++q) mx = fmaxf(mx, ml[(q * kThinRows + r) * 2]);
-      ms = mx == -INFINITY ? 0.f : mx;
+        for (int j = 0; j < NR; ++j) M::mma(o[j][d], va, pb[j][0], pb[j][1]);
+      }
+      __syncwarp();
+      if (i + kThinStages < mine) issue(i + kThinStages);
     }
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+
+    // the share's result, normalised by its own sum
+    const bool all = pg0 == 0 && share == pages;
+    const int slot = 2 * self + (x + first[e] == f0 ? 0 : 1);
 #pragma unroll
-    for (int q = 0; q < kThinWarps; ++q) {
-      const float f = exp2f(ml[(q * kThinRows + r) * 2] - ms);
-      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + q * L::WARP) + r * L::LDO + d);
-      sum += f * ml[(q * kThinRows + r) * 2 + 1];
-      a.x += f * v.x;
-      a.y += f * v.y;
-      a.z += f * v.z;
-      a.w += f * v.w;
-    }
-    const float* src = p.part_o + w.at * DH + d;
-#pragma unroll 8
-    for (int c = 0; c < parts; ++c) {
-      const float f = weights(r)[c];
-      const float4 v = *reinterpret_cast<const float4*>(src + c * R * DH);
-      sum += f;
-      a.x += f * v.x;
-      a.y += f * v.y;
-      a.z += f * v.z;
-      a.w += f * v.w;
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    const float lse2 = sum > 0.f ? ms + log2f(sum) : -INFINITY;
-    if (it.last) {
-      *reinterpret_cast<uint2*>(static_cast<T16*>(p.out) + w.at * DH + d) = make_uint2(M::pack(a.x, a.y), M::pack(a.z, a.w));
-      if (d == 0 && p.lse != nullptr) p.lse[w.at] = lse2 * 0.69314718055994531f;
-    } else {
-      *reinterpret_cast<float4*>(p.part_o + (out_chunk * R + w.at) * DH + d) = a;
-      if (d == 0) p.part_lse[out_chunk * R + w.at] = lse2;
-    }
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[j][h] += __shfl_xor_sync(0xffffffffu, l[j][h], w);
+        const int r = 8 * j + 2 * t4 + h;
+        const Row row = find_row(p, it, it.row0 + r);
+        if (!row.live) continue;
+        const long long at = all ? (it.shared ? 0 : R) + row.at : static_cast<long long>(slot) * p.thin_rows + r;
+        const float inv = l[j][h] > 0.f ? 1.f / l[j][h] : 0.f;
+        float* dst = (all ? p.whole_o : p.slot_o) + at * DH + gr;
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+          dst[16 * d] = o[j][d][h] * inv;
+          dst[16 * d + 8] = o[j][d][2 + h] * inv;
+        }
+        if (gr == 0) (all ? p.whole_lse : p.slot_lse)[at] = l[j][h] > 0.f ? m[j][h] + log2f(l[j][h]) : -INFINITY;
+      }
   }
-  pdl_wait();
+  if (!ok) {  // a wait gave up: what is still in flight gets its own bounded waits before the CTA leaves
+    for (int c = i; c < min(mine, i + kThinStages); ++c) mbar_wait(&bars[c % kThinStages], (c / kThinStages) & 1, p.status);
+  }
+  pdl_wait();  // (the joining kernel starts its work once all of this one has left, and what ran before it)
 }
 
 constexpr int kJoinWarps = 8;
 
-// out of the partial results, chunks in order: `share` warps (1 or 8) a query
-// row, each adding every share-th chunk.
+// out of the partial results: `share` warps (1 or 8) a query row, each adding
+// every share-th part.  Parts: of the prefix, then of the entry's own sequence;
+// the wide kernel leaves them by chunk, the thin one as said above.
 template <typename T16, int DH>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, int share) {
   using M = Mma16<T16>;
   constexpr int E = DH / 32;  // elements a lane
-  __shared__ float s_a[kJoinWarps][DH], s_sum[kJoinWarps];
+  __shared__ float s_a[kJoinWarps][DH], s_sum[kJoinWarps], s_top[kJoinWarps];
+  __shared__ long long s_first[kThinHeld + 1], s_scan[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % share;
   const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
   const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / share) + warp / share;
   const long long tok = row / p.Hq;
   const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+  const int h = static_cast<int>(row - tok * p.Hq), kvh = h / p.G;
   const bool live = row < R && t < entry_rows(p, b);
-  int n_pre = 0, n_all = 0;
+  // [0] the prefix's parts, [1] the own ones: how many, and where they are
+  int n[2] = {0, 0}, lane_row[2] = {0, 0};
+  long long f0[2] = {0, 0}, w0[2] = {0, 0};  // (thin) first page on the line, and the warp that takes it
+  long long per = 1;
+  Group g{0, 0, -1, 0, 0, 0};
+  int own = 0;
   if (live) {
-    n_pre = prefix_parts(p, b);
-    const int pages = (seq_tokens(p, p.seq != nullptr ? p.seq[b] : b) + kPage - 1) / kPage;
-    const int per = chunk_pages(pages, p.s_chunks);
-    n_all = n_pre + (pages + per - 1) / per;
+    g = group_of(p, b);
+    own = pages_of(seq_tokens(p, p.seq != nullptr ? p.seq[b] : b));
   }
-  pdl_wait();
+  // the thin kernel's line (a long one is read where that kernel left it)
+  const int groups = p.p_thin ? p.NG : 0;
+  const bool held = groups + p.B <= kThinHeld;
+  const long long* first = held ? s_first : p.work;
+  if (p.warps > 0 && held)
+    thin_line<kJoinWarps>(p, groups, p.NG == 0 || bounds_ok(p), false, s_first, nullptr, s_scan);
+  if (!held) pdl_wait();
+  if (live) {
+    const int pre = pages_of(g.tokens);
+    if (p.p_chunks > 0) n[0] = chunks_of(pre, p.p_chunks);
+    if (p.s_chunks > 0) n[1] = chunks_of(own, p.s_chunks);
+    if (p.warps > 0) per = thin_per(first[groups + p.B], p.warps);
+    auto on_line = [&](int which, int e, int pages, int r) {
+      f0[which] = first[e] + static_cast<long long>(r / p.thin_rows * p.Hkv + kvh) * pages;
+      w0[which] = thin_div(f0[which], per);
+      lane_row[which] = r % p.thin_rows;
+      n[which] = pages > 0 ? static_cast<int>(thin_div(f0[which] + pages - 1, per) - w0[which]) + 1 : 0;
+    };
+    const int gi = h - kvh * p.G;
+    if (p.p_thin && pre > 0) on_line(0, g.index, pre, ((b - g.lo) * p.T + t) * p.G + gi);
+    if (p.s_chunks == 0) on_line(1, groups + b, own, t * p.G + gi);
+  }
+  const int n_all = n[0] + n[1];
+  // where part c is: its log-sum-exp, and its output
+  auto place = [&](int c, const float*& lse, const float*& o) {
+    const int which = c < n[0] ? 0 : 1, k = which ? c - n[0] : c;
+    long long at;
+    if (which ? p.s_chunks > 0 : p.p_chunks > 0) {
+      at = static_cast<long long>(which ? p.p_chunks + k : k) * R + row;
+      lse = p.part_lse;
+      o = p.part_o;
+    } else if (n[which] == 1) {
+      at = which * R + row;
+      lse = p.whole_lse;
+      o = p.whole_o;
+    } else {
+      const long long w = w0[which] + k;
+      at = (2 * w + (k > 0 || f0[which] == w * per ? 0 : 1)) * p.thin_rows + lane_row[which];
+      lse = p.slot_lse;
+      o = p.slot_o;
+    }
+    lse += at;
+    o += at * DH;
+  };
+  // kJoinParts parts at a time: a lane finds one and its weight, then all add
+  // them up.  What they need from before is found first, so that one wait for
+  // memory is left once the partial results are there.
+  constexpr int kJoinParts = 16;
   float mx = -INFINITY, sum = 0.f, a[E] = {};
-  auto place = [&](int c) { return static_cast<long long>(c < n_pre ? c : p.p_chunks + c - n_pre) * R + row; };
-  for (int c = lane; c < n_all; c += 32) mx = fmaxf(mx, p.part_lse[place(c)]);
-  mx = warp_max(mx);
-  const float ms = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-  for (int c = sub; c < n_all; c += share) {
-    const long long at = place(c);
-    const float f = exp2f(p.part_lse[at] - ms);
-    const float* src = p.part_o + at * DH + lane * E;
-    float v[E];
-    if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+  for (int c0 = 0; c0 * share + sub < n_all || c0 == 0; c0 += kJoinParts) {
+    const int c = (c0 + (lane & (kJoinParts - 1))) * share + sub;
+    const int count = min(kJoinParts, (n_all - sub + share - 1) / share - c0);
+    const float *lse = nullptr, *mine = nullptr;
+    if (c < n_all) place(c, lse, mine);
+    const unsigned long long addr = reinterpret_cast<unsigned long long>(mine);
+    if (c0 == 0 && held) pdl_wait();
+    const float z = c < n_all && lane < kJoinParts ? *lse : -INFINITY;
+    float v[kJoinParts][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) a[e] += f * v[e];
-    sum += f;
+    for (int k = 0; k < kJoinParts; ++k) {
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, k)) + lane * E;
+      if (k >= count) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+      } else if constexpr (E == 4) {
+        *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+      } else {
+        *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+      }
+    }
+    const float top = fmaxf(mx, warp_max(z)), at = top == -INFINITY ? 0.f : top;
+    const float keep = exp2f(mx - at), f = exp2f(z - at);
+    mx = top;
+    sum = sum * keep + warp_sum(f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < kJoinParts; ++k) {
+      const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] += w * v[k][e];
+    }
   }
   if (share > 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) s_a[warp][lane * E + e] = a[e];
-    if (lane == 0) s_sum[warp] = sum;
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_top[warp] = mx;
+    }
     __syncthreads();
     if (warp != 0) return;
+    for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, s_top[w]);
+    const float at = mx == -INFINITY ? 0.f : mx;
+    sum = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] = 0.f;
-    sum = 0.f;
-    for (int w = 0; w < kJoinWarps; ++w) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] += s_a[w][lane * E + e];
-      sum += s_sum[w];
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = exp2f(s_top[w] - at);
+      sum += f * s_sum[w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] += f * s_a[w][lane * E + e];
     }
   }
+  const float ms = mx == -INFINITY ? 0.f : mx;
   if (!live) return;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   T16* dst = static_cast<T16*>(p.out) + row * DH + lane * E;
@@ -374,12 +535,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 constexpr int kWideFrom = 48;
 
 struct PrefixPlan {
-  bool p_wide, s_wide;         // whether the wide kernel takes the part (else the thin one)
-  bool merge;                  // own parts add the prefix's partial results
-  long long p_tiles, s_tiles;  // row tiles: of all groups (a bound), of an entry
+  bool p_wide, s_wide;         // whether the wide kernel takes the prefix, the own parts (else the thin one)
+  bool merge, join;            // own parts add the prefix's partial results; a kernel joins them all
+  long long p_tiles, s_tiles;  // row tiles of the wide kernel: of all groups (a bound), of an entry
   long long rows;
-  int p_chunks, s_chunks;
-  size_t off_lse, bytes;
+  int p_chunks, s_chunks;      // of the wide kernel's parts (0: the thin kernel's)
+  int warps, thin_rows;        // of the thin kernel (0: not used): warps, and query rows of a tile (8 or 16)
+  size_t off_work, off_lse, off_o, off_whole_lse, off_whole_o, off_slot_lse, off_slot_o, bytes;
 };
 
 int plan_sms() {
@@ -392,15 +554,20 @@ int plan_sms() {
   return n;
 }
 
-// Chunks per item: the count whose waves of CTAs (`slots` at once) take the
-// least time, a CTA costing its steps (of `step` pages) and `start` more to
-// start and to write its rows, and a part in several chunks `join` more.
-int plan_chunks(long long items, int tokens, long long slots, int step, int start, int join, int most) {
-  const int steps = std::max(1, (tokens + step * kPage - 1) / (step * kPage));
+// Chunks of a wide item: the count that takes the least time on `slots` CTAs
+// at once, a CTA costing its key tiles and about three more to start and to
+// write its rows.  Items of one length run in waves; of several (the mean taken
+// as 0.6 of the longest) they fill the slots and leave the longest as a tail.
+int plan_chunks(long long items, int tokens, long long slots, bool even, double join) {
+  const int tiles = std::max(1, (tokens + 127) / 128);
   int best = 1;
-  long long cost = INT64_MAX;
-  for (int c = 1; c <= std::min(steps, most); ++c) {
-    const long long t = (items * c + slots - 1) / slots * ((steps + c - 1) / c + start) + (c > 1 ? join : 0);
+  double cost = 1e300;
+  for (int c = 1; c <= std::min(tiles, 64); ++c) {
+    const double per = (tiles + c - 1) / c + 3, n = static_cast<double>(items) * c / slots;
+    double t = per;
+    if (n > 1 && even) t = static_cast<double>((items * c + slots - 1) / slots) * per;
+    else if (n > 1) t = n * (0.6 * tiles / c + 3) + per;
+    if (c > 1) t += join;
     if (t < cost) {
       cost = t;
       best = c;
@@ -410,33 +577,56 @@ int plan_chunks(long long items, int tokens, long long slots, int step, int star
 }
 
 bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_prefix, int max_len, PrefixPlan* out) {
-  const int G = Hq / kv.n_kv_heads;
+  const int G = Hq / kv.n_kv_heads, Hkv = kv.n_kv_heads;
   const long long tg = static_cast<long long>(T) * G;
   const int cap = kv.max_pages * kPage;
   const int mp = max_prefix > 0 ? std::min(max_prefix, cap) : cap, ml = max_len > 0 ? std::min(max_len, cap) : cap;
   PrefixPlan r{};
   r.rows = static_cast<long long>(B) * T * Hq;
   const bool fits = G <= kWideTile;  // (a token's heads stay in one row tile)
-  r.p_wide = fits && NG > 0 && B * tg >= static_cast<long long>(kWideFrom) * NG;
   r.s_wide = fits && tg >= kWideFrom;
-  const int p_rows = r.p_wide ? wide_rows(G) : kThinRows;
-  const int s_rows = r.s_wide ? wide_rows(G) : kThinRows;
-  r.p_tiles = NG > 0 ? (B * tg + static_cast<long long>(NG) * (p_rows - 1)) / p_rows : 0;
-  r.s_tiles = (tg + s_rows - 1) / s_rows;
-  const int sms = plan_sms(), thin_slots = sms * (kv.head_dim == 64 ? 4 : 2);
-  const long long p_items = r.p_tiles * kv.n_kv_heads, s_items = B * r.s_tiles * kv.n_kv_heads;
-  const auto chunks = [&](bool wide, long long items, int tokens, int join) {
-    return wide ? plan_chunks(items, tokens, 2 * sms, kMinChunkPages, 3, join, kMaxParts / 2)
-                : plan_chunks(items, tokens, thin_slots, kMinChunkPages, 2, join, kMaxParts);
+  r.p_wide = fits && NG > 0 && (r.s_wide || B * tg >= static_cast<long long>(kWideFrom) * NG);
+  const int sms = plan_sms(), rows = wide_rows(std::min(G, kWideTile));
+  if (r.p_wide) {
+    r.p_tiles = (B * tg + static_cast<long long>(NG) * (rows - 1)) / rows;
+    // (beside the thin kernel, which waits for memory, one CTA an SM)
+    r.p_chunks = plan_chunks(r.p_tiles * Hkv, mp, r.s_wide ? 2 * sms : sms, NG == 1, 0);
+  }
+  if (r.s_wide) {
+    r.s_tiles = (tg + rows - 1) / rows;
+    r.s_chunks = plan_chunks(B * r.s_tiles * Hkv, ml, 2 * sms, B == 1, 4);
+    // (a wide own part adds a row's copies one after the other)
+    r.merge = NG > 0 && r.s_chunks == 1 && r.p_chunks <= 4;
+    r.join = r.s_chunks > 1 || (NG > 0 && !r.merge);
+  } else {
+    // as many warps as the SMs hold, or as there can be shares of kThinPages pages
+    r.thin_rows = tg <= 8 && (NG == 0 || r.p_wide || B * tg <= 8 * static_cast<long long>(NG)) ? 8 : 16;
+    const auto tiles = [&](long long n) { return (n + r.thin_rows - 1) / r.thin_rows; };
+    const long long line = B * tiles(tg) * Hkv * ((ml + kPage - 1) / kPage) +
+                           (NG > 0 && !r.p_wide ? (tiles(B * tg) + NG) * Hkv * ((mp + kPage - 1) / kPage) : 0);
+    // (beside the wide kernel's CTAs half of them: all of a line's warps start at once)
+    const long long most = static_cast<long long>(sms) * (kv.head_dim == 64 ? 4 : 2) / (r.p_wide ? 2 : 1) * kThinWarps;
+    const long long want = (line + kThinPages - 1) / kThinPages;
+    r.warps = static_cast<int>(std::min(most, (want + kThinWarps - 1) / kThinWarps * kThinWarps));
+    r.join = true;
+  }
+  if (r.p_tiles * Hkv * r.p_chunks > INT32_MAX || B * r.s_tiles * Hkv * r.s_chunks > INT32_MAX) return false;
+  const size_t parts = r.join || r.merge ? r.p_chunks + (r.join ? r.s_chunks : 0) : 0;
+  const size_t dh = kv.head_dim, whole = r.warps > 0 ? 2 * r.rows : 0, slots = 2ull * r.warps * r.thin_rows;
+  size_t off = 256;  // (the first 256 bytes: a status word for callers without one)
+  const auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
   };
-  r.p_chunks = NG == 0 ? 0 : chunks(r.p_wide, p_items, mp, 0);
-  r.s_chunks = chunks(r.s_wide, s_items, ml, 3);
-  // (a wide own part adds a row's copies one after the other)
-  r.merge = NG > 0 && r.s_chunks == 1 && !(r.s_wide && r.p_chunks > 4);
-  if (p_items * r.p_chunks + s_items * r.s_chunks > INT32_MAX) return false;
-  const int parts = r.p_chunks + (r.merge || (NG == 0 && r.s_chunks == 1) ? 0 : r.s_chunks);
-  r.off_lse = 256;  // (the first 256 bytes: a status word for callers without one)
-  r.bytes = r.off_lse + (sizeof(float) * r.rows * parts + 255) / 256 * 256 + sizeof(float) * r.rows * parts * kv.head_dim;
+  r.off_work = take(r.warps > 0 ? 8 * (static_cast<size_t>(NG) + B + 1) : 0);
+  r.off_lse = take(4 * r.rows * parts);
+  r.off_whole_lse = take(4 * whole);
+  r.off_slot_lse = take(4 * slots);
+  r.off_o = take(4 * r.rows * parts * dh);
+  r.off_whole_o = take(4 * whole * dh);
+  r.off_slot_o = take(4 * slots * dh);
+  r.bytes = off;
   *out = r;
   return true;
 }
@@ -447,20 +637,22 @@ dflash_status check_prefix(const dflash_paged_kv* kv, int Hq, int B, int T, int 
   if (Hq % kv->n_kv_heads) return DFLASH_ERR_INVALID_ARG;
   if (kv->elem == DFLASH_ELEM_F32 || (kv->head_dim != 64 && kv->head_dim != 128)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
   // row counts stay well inside 32 bits
-  if (static_cast<long long>(B) * T * Hq > INT32_MAX / 2 || NG > (1 << 20))
+  if (static_cast<long long>(B) * T * Hq > INT32_MAX / 2 || B > kMaxEntries || NG > kMaxEntries)
     return DFLASH_ERR_UNSUPPORTED_SHAPE;
   return DFLASH_OK;
 }
 
-// Pages of one layer as a 4-D map with boxes of 16 tokens x 64 elements (128-byte swizzled rows).
-bool page_map(const dflash_paged_kv& kv, void* base, CUtensorMap* out) {
+// Pages of one layer as a 5-D map (64 elements, token, chunk of 64, head, page)
+// with boxes of 16 tokens x `chunks` chunks (128-byte swizzled rows).
+bool page_map(const dflash_paged_kv& kv, void* base, int chunks, CUtensorMap* out) {
   const auto fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   const cuuint64_t dh = kv.head_dim;
-  const cuuint64_t gdim[4] = {dh, kPage, static_cast<cuuint64_t>(kv.n_kv_heads), static_cast<cuuint64_t>(kv.n_pages)};
-  const cuuint64_t gstride[3] = {dh * 2, dh * 2 * kPage, dh * 2 * kPage * kv.n_kv_heads};
-  const cuuint32_t box[4] = {64, kPage, 1, 1}, es[4] = {1, 1, 1, 1};
-  return fn(out, kv.elem == DFLASH_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+  const cuuint64_t gdim[5] = {64, kPage, dh / 64, static_cast<cuuint64_t>(kv.n_kv_heads),
+                              static_cast<cuuint64_t>(kv.n_pages)};
+  const cuuint64_t gstride[4] = {dh * 2, 128, dh * 2 * kPage, dh * 2 * kPage * kv.n_kv_heads};
+  const cuuint32_t box[5] = {64, kPage, static_cast<cuuint32_t>(chunks), 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return fn(out, kv.elem == DFLASH_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
             base, gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -480,32 +672,36 @@ bool query_map(const dflash_paged_kv& kv, const void* q, int Hq, long long token
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T16, int DH>
-cudaError_t launch_thin(const PrefixParams& p, long long n_prefix, long long n_own, bool behind, const CUtensorMap& tk,
-                        const CUtensorMap& tv, cudaStream_t s) {
+struct PrefixMaps {
+  CUtensorMap q, wide_k, wide_v, thin_k, thin_v;
+};
+
+template <typename T16, int DH, int NR>
+cudaError_t launch_thin(const PrefixParams& p, bool behind, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t s) {
+  const int line = (p.p_thin ? p.NG : 0) + p.B;
+  const int smem = ThinLayout<DH>::SMEM + (line + 2) / 2 * 16 + (line <= kThinHeld ? line * 16 : 0);
   static FuncAttr attr;
-  const cudaError_t e = attr.ensure(ThinLayout<DH>::SMEM, [](int v) {
-    return cudaFuncSetAttribute(k_prefix_thin<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+  const cudaError_t e = attr.ensure(smem, [](int v) {
+    return cudaFuncSetAttribute(k_prefix_thin<T16, DH, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
   });
   if (e != cudaSuccess) return e;
-  return launch_k(k_prefix_thin<T16, DH>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(kThinThreads),
-                  ThinLayout<DH>::SMEM, s, dim3(1), behind, tk, tv, p, static_cast<int>(n_prefix));
+  return launch_k(k_prefix_thin<T16, DH, NR>, dim3(p.warps / kThinWarps), dim3(kThinThreads), smem, s, dim3(1), behind,
+                  tk, tv, p);
 }
 
 template <typename T16, int DH>
-cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int elem, const CUtensorMap& tq,
-                          const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int elem, const PrefixMaps& m, cudaStream_t s) {
   const long long n_prefix = plan.p_tiles * plan.p_chunks * p.Hkv, n_own = p.B * plan.s_tiles * plan.s_chunks * p.Hkv;
   cudaError_t e = cudaSuccess;
-  if (n_prefix > 0)
-    e = plan.p_wide ? launch_prefix_wide(p, elem, DH, n_prefix, 0, false, tq, tk, tv, s)
-                    : launch_thin<T16, DH>(p, n_prefix, 0, false, tk, tv, s);
+  if (plan.p_wide) e = launch_prefix_wide(p, elem, DH, n_prefix, 0, false, m.q, m.wide_k, m.wide_v, s);
   if (e == cudaSuccess)
-    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, 0, n_own, n_prefix > 0, tq, tk, tv, s)
-                    : launch_thin<T16, DH>(p, 0, n_own, n_prefix > 0, tk, tv, s);
-  if (e != cudaSuccess || p.merge || (p.NG == 0 && p.s_chunks == 1)) return e;
-  // few rows of many parts: a row's parts over all the warps of a CTA
-  const int share = p.p_chunks + p.s_chunks >= 16 ? kJoinWarps : 1, per = kJoinWarps / share;
+    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, 0, n_own, plan.p_wide, m.q, m.wide_k, m.wide_v, s)
+                    : plan.thin_rows == 8 ? launch_thin<T16, DH, 1>(p, plan.p_wide, m.thin_k, m.thin_v, s)
+                            : launch_thin<T16, DH, 2>(p, plan.p_wide, m.thin_k, m.thin_v, s);
+  if (e != cudaSuccess || !plan.join) return e;
+  // few rows: a row's parts over all the warps of a CTA
+  const int share = plan.rows < 8ll * 152 ? kJoinWarps : 1, per = kJoinWarps / share;
   return launch_k(k_prefix_join<T16, DH>, dim3(static_cast<unsigned>((plan.rows + per - 1) / per)),
                   dim3(kJoinWarps * 32), 0, s, dim3(1), true, p, share);
 }
@@ -559,9 +755,12 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   if (!make_plan(*kv, n_q_heads, B, T, NG, max_prefix, max_len, &plan)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
   if (workspace_bytes < plan.bytes) return DFLASH_ERR_WORKSPACE;
   const long long ldq = one ? qd : ld_q;
-  CUtensorMap tq{}, tk, tv;
-  if (!page_map(*kv, kv->k, &tk) || !page_map(*kv, kv->v, &tv) ||
-      ((plan.p_wide || plan.s_wide) && !query_map(*kv, q, n_q_heads, static_cast<long long>(B) * T, ldq, &tq)))
+  PrefixMaps maps{};
+  const int chunks = kv->head_dim / 64;
+  if ((plan.warps > 0 && (!page_map(*kv, kv->k, chunks, &maps.thin_k) || !page_map(*kv, kv->v, chunks, &maps.thin_v))) ||
+      ((plan.p_wide || plan.s_wide) &&
+       (!page_map(*kv, kv->k, 1, &maps.wide_k) || !page_map(*kv, kv->v, 1, &maps.wide_v) ||
+        !query_map(*kv, q, n_q_heads, static_cast<long long>(B) * T, ldq, &maps.q))))
     return DFLASH_ERR_CUDA;
   PrefixParams p{};
   p.q = q;
@@ -587,9 +786,16 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.merge = plan.merge;
-  const int parts = plan.p_chunks + (plan.merge ? 0 : plan.s_chunks);
+  p.p_thin = NG > 0 && !plan.p_wide;
+  p.work = reinterpret_cast<long long*>(ws + plan.off_work);
   p.part_lse = reinterpret_cast<float*>(ws + plan.off_lse);
-  p.part_o = reinterpret_cast<float*>(ws + plan.off_lse + (sizeof(float) * plan.rows * parts + 255) / 256 * 256);
+  p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
+  p.whole_lse = reinterpret_cast<float*>(ws + plan.off_whole_lse);
+  p.whole_o = reinterpret_cast<float*>(ws + plan.off_whole_o);
+  p.slot_lse = reinterpret_cast<float*>(ws + plan.off_slot_lse);
+  p.slot_o = reinterpret_cast<float*>(ws + plan.off_slot_o);
+  p.warps = plan.warps;
+  p.thin_rows = plan.thin_rows;
   p.status = status != nullptr ? status : reinterpret_cast<int*>(ws);
   p.p_tiles = static_cast<int>(plan.p_tiles);
   p.p_chunks = plan.p_chunks;
@@ -597,11 +803,11 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.s_chunks = plan.s_chunks;
   cudaError_t e;
   if (kv->elem == DFLASH_ELEM_BF16)
-    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, plan, kv->elem, tq, tk, tv, stream)
-                           : launch_prefix<__nv_bfloat16, 128>(p, plan, kv->elem, tq, tk, tv, stream);
+    e = kv->head_dim == 64 ? launch_prefix<__nv_bfloat16, 64>(p, plan, kv->elem, maps, stream)
+                           : launch_prefix<__nv_bfloat16, 128>(p, plan, kv->elem, maps, stream);
   else
-    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, plan, kv->elem, tq, tk, tv, stream)
-                           : launch_prefix<__half, 128>(p, plan, kv->elem, tq, tk, tv, stream);
+    e = kv->head_dim == 64 ? launch_prefix<__half, 64>(p, plan, kv->elem, maps, stream)
+                           : launch_prefix<__half, 128>(p, plan, kv->elem, maps, stream);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

@@ -26,6 +26,12 @@ struct PrefixParams {
   int p_tiles, p_chunks;  // prefix parts: row tiles over all groups (a bound), chunks of pages
   int s_tiles, s_chunks;  // own parts: row tiles of an entry, chunks of pages
   bool merge;             // own parts (of one chunk) add the prefix's partial results and write the result
+  bool p_thin;            // the thin kernel takes the prefix parts (no p_chunks then)
+  // what the thin kernel leaves for the joining one (ThinWork)
+  long long* work;                // [NG] + [B] first pages, then pages a warp
+  float *whole_lse, *whole_o;     // [2][B*T*Hq], [..][DH]: prefix and own parts that one warp took whole
+  float *slot_lse, *slot_o;       // [2 * warps][thin_rows], [..][DH]: a warp's first and last part, where others share them
+  int warps, thin_rows;           // its warps, and the query rows of its tiles
 };
 
 // Chunks are whole multiples of this many pages (a key tile of the wide
@@ -56,6 +62,7 @@ struct Group {
   int row;      // the prefix's sequence (-1: none)
   int tokens;   // and length
   int tile;     // row tile within the group
+  int index;
 };
 
 __device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
@@ -65,6 +72,7 @@ __device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
   r.row = p.prefix_seq[g];
   r.tokens = seq_tokens(p, r.row);
   r.tile = 0;
+  r.index = g;
   return r;
 }
 
@@ -114,14 +122,33 @@ __device__ __forceinline__ Group find_entry(const PrefixParams& p, int b) {
     const unsigned in = __ballot_sync(0xffffffffu, g < p.NG && b >= p.group_off[g] && b < p.group_off[g + 1]);
     if (in != 0) return load_group(p, g0 + __ffs(in) - 1);
   }
-  return Group{0, 0, -1, 0, 0};
+  return Group{0, 0, -1, 0, 0, 0};
 }
 
-// How many partial results entry b has of its prefix (the whole warp asks).
-__device__ __forceinline__ int prefix_parts(const PrefixParams& p, int b) {
-  if (p.NG == 0 || !bounds_ok(p)) return 0;
-  const int pages = (find_entry(p, b).tokens + kPage - 1) / kPage, per = chunk_pages(pages, p.p_chunks);
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+
+// The group of entry b where the bounds are sound (the whole warp asks).
+__device__ __forceinline__ Group group_of(const PrefixParams& p, int b) {
+  return p.NG > 0 && bounds_ok(p) ? find_entry(p, b) : Group{0, 0, -1, 0, 0, 0};
+}
+
+// Chunks that hold `pages` pages (chunks > 0).
+__device__ __forceinline__ int chunks_of(int pages, int chunks) {
+  const int per = chunk_pages(pages, chunks);
   return (pages + per - 1) / per;
+}
+
+__device__ __forceinline__ void check_prefix(const PrefixParams& p, int row) {
+  if (row == -1) return;
+  if (row < -1 || row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
+  else if (p.seq_len[row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
+}
+
+__device__ __forceinline__ void check_entry(const PrefixParams& p, int b, int row) {
+  const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
+  if (n < 0 || n > p.T) flag_status(p.status, ST_BAD_ROWS);
+  if (row < 0 || row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
+  else if (p.seq_len[row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
 }
 
 // What one CTA works on: a tile of query rows of one kv head over a chunk of pages.
@@ -156,10 +183,7 @@ __device__ __forceinline__ bool find_item(const PrefixParams& p, int index, int 
     it.rows = (g.hi - g.lo) * p.T * p.G;
     it.tokens = g.tokens;
     it.table_row = g.row;
-    if (first && g.row != -1) {
-      if (g.row < -1 || g.row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
-      else if (p.seq_len[g.row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
-    }
+    if (first) check_prefix(p, g.row);
   } else {
     const int b = tile / p.s_tiles;
     it.b0 = b;
@@ -170,16 +194,10 @@ __device__ __forceinline__ bool find_item(const PrefixParams& p, int index, int 
     if (p.NG > 0 && b == 0 && it.row0 == 0 && it.kvh == 0 && it.chunk == 0 && threadIdx.x < 32 && !bounds_ok(p) &&
         threadIdx.x == 0)
       flag_status(p.status, ST_BAD_BLOCK);
-    if (first && it.row0 == 0) {
-      const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
-      if (n < 0 || n > p.T) flag_status(p.status, ST_BAD_ROWS);
-      if (it.table_row < 0 || it.table_row >= p.n_seqs) flag_status(p.status, ST_BAD_BLOCK);
-      else if (p.seq_len[it.table_row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
-    }
+    if (first && it.row0 == 0) check_entry(p, b, it.table_row);
   }
   if (it.row0 >= it.rows) return false;
-  const int pages = (it.tokens + kPage - 1) / kPage;
-  const int per = chunk_pages(pages, chunks);
+  const int pages = pages_of(it.tokens), per = chunk_pages(pages, chunks);
   it.pg0 = it.chunk * per;
   it.pg1 = min(pages, it.pg0 + per);
   it.last = !it.shared && (p.merge || (p.NG == 0 && p.s_chunks == 1));
@@ -239,12 +257,22 @@ struct Mma16<__half> {
   }
 };
 
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int page) {
+// One head's 16 tokens of a page, from 64-element chunk c on (the map says how
+// many chunks: [chunk][16 tokens][128 bytes], swizzled).
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c, int h, int page) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(h), "r"(page), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c), "r"(h), "r"(page), "r"(smem_u32(bar))
       : "memory");
+}
+// One thread of a converged warp, the same one every time.  Copies and MMAs
+// take their operands from uniform registers: where the whole warp computes
+// them alike and one thread is elected to issue, they are there already.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+  return is != 0;
 }
 
 // prefix_wide.cu: items of a tile of wide_rows(G) query rows (whole tokens),

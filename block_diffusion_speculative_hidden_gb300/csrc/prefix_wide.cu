@@ -61,12 +61,6 @@ template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// One thread of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
-  return is != 0;
-}
 __device__ __forceinline__ void wide_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -166,49 +160,58 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
   if (warp >= L::SOFT) {
     regs_down<L::FEED_REGS>();
     if (warp == kTmaWarp) {
-      // ---------------- Q, then K and V tiles: lane l fetches chunk l % NCH of page l / NCH
+      // ---------------- Q, then K and V tiles: lane l has the ids of page l % 8 of four tiles
+      const int key_tiles = __shfl_sync(0xffffffffu, n, 0), pages = __shfl_sync(0xffffffffu, np, 0);
+      const int kvh = __shfl_sync(0xffffffffu, it.kvh, 0);
       const int32_t* table = p.page_table + static_cast<long long>(it.table_row) * p.max_pages + it.pg0;
-      const int pg = lane / L::NCH, c = lane % L::NCH;
-      auto page_id = [&](int j) {
-        const int i = j * kWidePages + pg;
+      const bool elected = elect_one();
+      auto page_ids = [&](int i0) {
         int id = 0;
-        if (pg < kWidePages && i < np) {
-          id = table[i];
+        if (i0 + lane < np) {
+          id = table[i0 + lane];
           if (id < 0 || id >= p.n_pages) {
-            if (c == 0) flag_status(p.status, ST_BAD_PAGE);
+            flag_status(p.status, ST_BAD_PAGE);
             id = p.n_pages;  // outside the tensor map: reads as zeros
           }
         }
         return id;
       };
-      int next = n > 0 ? page_id(0) : 0, issued = 0;
+      int ids = page_ids(0), next = page_ids(32), issued = 0;
       bool ok = true;
-      if (lane == 0 && n > 0) {
+      if (elected && key_tiles > 0) {
         // whole tokens: a tile's first row is a token's first head of the group
         mbar_arrive_expect_tx(q_full, rows_tile * L::NCH * 128);
         for (int cc = 0; cc < L::NCH; ++cc)
           tma_rows(smem_u32(smem + cc * L::Q_CH), &tmQ, q_full, cc * 64, it.kvh * p.G, it.b0 * p.T + it.row0 / p.G);
       }
-      for (int j = 0; ok && j < n; ++j) {
-        const int id = next, npb = min(kWidePages, np - j * kWidePages);
-        if (j + 1 < n) next = page_id(j + 1);
-        for (int kv = 0; kv < 2 && ok; ++kv) {
+      for (int j = 0; ok && j < key_tiles; ++j) {
+        const int npb = min(kWidePages, pages - j * kWidePages);
+        if (j > 0 && j % 4 == 0) {
+          ids = next;
+          next = page_ids((j + 4) * kWidePages);
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
           const int i = 2 * j + kv, s = i % L::NS;
-          if (lane == 0) {
-            if (i >= L::NS) ok = mbar_wait(&kv_empty[s], (i / L::NS - 1) & 1, p.status);
-            if (ok) mbar_arrive_expect_tx(&kv_full[s], npb * L::NCH * 2048);
+          if (ok && i >= L::NS)
+            ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[s], (i / L::NS - 1) & 1, p.status)) != 0;
+          if (!ok) break;
+          if (elected) mbar_arrive_expect_tx(&kv_full[s], npb * L::NCH * 2048);
+          const uint32_t dst = smem_u32(smem + L::OFF_KV) + s * L::SLOT;
+#pragma unroll
+          for (int g = 0; g < kWidePages; ++g) {
+            const int id = __shfl_sync(0xffffffffu, ids, j % 4 * kWidePages + g);
+            if (g < npb && elected) {
+#pragma unroll
+              for (int cc = 0; cc < L::NCH; ++cc)
+                tma_page(dst + cc * L::KV_CH + g * 2048, kv ? &tmV : &tmK, &kv_full[s], cc, kvh, id);
+            }
           }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (ok) {
-            if (pg < npb)
-              tma_page(smem_u32(smem + L::OFF_KV + s * L::SLOT + c * L::KV_CH + pg * 2048), kv ? &tmV : &tmK,
-                       &kv_full[s], c * 64, it.kvh, id);
-            issued = i + 1;
-          }
+          issued = i + 1;
         }
       }
       // every copy has landed before the CTA may leave
-      if (lane == 0 && n > 0) mbar_wait(q_full, 0, p.status);
+      if (key_tiles > 0) mbar_wait(q_full, 0, p.status);
       for (int i = max(0, issued - L::NS); i < issued; ++i) mbar_wait(&kv_full[i % L::NS], (i / L::NS) & 1, p.status);
     } else if (warp == kMmaWarp) {
       // ---------------- MMAs.  Where P lies over S, S(j + 1) waits for P(j) V,
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     const int pair = 1 + quad;  // the named barrier of the row's two warps
     Row row = find_row(p, it, it.row0 + r);
     row.live = row.live && r < rows_tile;
-    const int parts = it.last && p.merge ? prefix_parts(p, it.b0) : 0;  // of the prefix, to be added at the end
+    const int parts = it.last && p.merge ? chunks_of(pages_of(group_of(p, it.b0).tokens), p.p_chunks) : 0;  // of the prefix, to be added at the end
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_at = tmem + lanes + L::S_COL + 64 * half, p_at = tmem + lanes + L::P_COL + 4 * L::P_PAGE * half;
     const uint32_t o_at = tmem + lanes + L::O_COL + DH / 2 * half;

@@ -493,8 +493,8 @@ dflash_status dflash_append_kv(const dflash_paged_kv* kv, const void* k, long lo
  * 16 * max_pages (SEQ_TOO_LONG) or a bad page (BAD_PAGE) sets its bit in
  * *status (device int32; NULL: not reported) and is read as n = 0, as length
  * 0, as its first 16 * max_pages tokens and as a page of zeros.
- * Asynchronous, allocates nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
- * WORKSPACE, CUDA. */
+ * Asynchronous, allocates nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE
+ * (also B or NG above 4096, or 2^30 rows and more), WORKSPACE, CUDA. */
 dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, long long ld_q, int n_q_heads,
                                       const int32_t* n_rows, const int32_t* seq, int B, int T,
                                       const int32_t* group_off, const int32_t* prefix_seq, int NG, int causal,
