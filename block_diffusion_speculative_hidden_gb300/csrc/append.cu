@@ -12,25 +12,34 @@ namespace dflash {
 
 namespace {
 
-// Eight elements of a row in registers as fp32.  vec: the address is
-// 16-byte aligned, so they come and go as 128-bit accesses.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
-  if (vec) {
-    constexpr int W = 16 / sizeof(T);  // elements per 128-bit access
+// Eight elements of a row as they are stored.  VEC: the address is 16-byte
+// aligned and they come as 128-bit loads, which stay where they are written:
+// before the waits for what decides where the row goes.
+template <typename T, bool VEC>
+struct Raw8 {
+  static constexpr int W = 16 / sizeof(T);  // elements per 128-bit access
+  union {
+    uint4 u[8 / W];
+    T t[8];
+  };
+  __device__ __forceinline__ Raw8() {}
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < 8 / W; ++j) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p + j * W);
-      T t[W];
-      memcpy(t, &u, 16);
+      for (int j = 0; j < 8 / W; ++j)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[j].x), "=r"(u[j].y), "=r"(u[j].z), "=r"(u[j].w)
+                     : "l"(p + j * W));
+    } else {
 #pragma unroll
-      for (int k = 0; k < W; ++k) x[j * W + k] = to_f32<T>(t[k]);
+      for (int k = 0; k < 8; ++k) t[k] = p[k];
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = to_f32<T>(p[k]);
   }
-}
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = to_f32<T>(t[k]);
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ T round_to(float v);
@@ -63,25 +72,27 @@ struct AppendParams {
   const int32_t *n_rows, *seq, *pos_base, *page_table, *seq_len;
   const float *rope_cos, *rope_sin;
   int rope_rows, B, T, Hq, Hkv, n_pages, n_seqs, max_pages;
-  bool vec_k, vec_v, vec_q;
   int* status;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendHeads = 2;  // (1: 9.2 us for verified blocks, 2: 8.3, 4: 9.6, for their registers)
 
-// A unit is one head of one row: DH / 16 threads, each with eight elements
-// of the head's first half and the eight they rotate with.
-template <typename S, typename D, int DH>
+// DH / 16 threads take kAppendHeads heads of one row, each eight elements of
+// the heads' first halves and the eight that they rotate with: the angles are
+// read once for those heads, and their elements are on the way while the
+// thread finds the row's slot.
+template <typename S, typename D, int DH, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams p) {
   constexpr int TPU = DH / 16, HALF = DH / 2;
-  const int heads = p.Hq + 2 * p.Hkv;
+  const int heads = p.Hq + 2 * p.Hkv, units = (heads + kAppendHeads - 1) / kAppendHeads;
   const long long u = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) / TPU;
   const int d = (threadIdx.x % TPU) * 8;
-  const long long row = u / heads;
+  const long long row = u / units;
   if (row >= static_cast<long long>(p.B) * p.T) return;
-  const int h = static_cast<int>(u - row * heads);
+  const int h0 = static_cast<int>(u - row * units) * kAppendHeads;
   const int b = static_cast<int>(row / p.T), i = static_cast<int>(row - static_cast<long long>(b) * p.T);
-  const bool first = h == 0 && d == 0;  // the thread that reports
+  const bool first = h0 == 0 && d == 0;  // the thread that reports
   auto flag = [&](int bit) {
     if (first && p.status != nullptr) atomicOr(p.status, bit);
   };
@@ -93,66 +104,76 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams p)
   if (bad) return flag(bad);
   if (i >= n) return;
   const int len = p.seq_len[s];
+  Raw8<S, VEC> raw[kAppendHeads][2];
+#pragma unroll
+  for (int j = 0; j < kAppendHeads; ++j) {
+    const int h = min(h0 + j, heads - 1), hk = h - p.Hq;
+    const S* src = hk < 0        ? static_cast<const S*>(p.q) + row * p.ld_q + h * DH
+                   : hk < p.Hkv ? static_cast<const S*>(p.k) + row * p.ld_k + hk * DH
+                                : static_cast<const S*>(p.v) + row * p.ld_v + (hk - p.Hkv) * DH;
+    raw[j][0].load(src + d);
+    raw[j][1].load(src + HALF + d);
+  }
   if (len < n) return flag(ST_BAD_ROWS);
   if (len > p.max_pages * kPage) return flag(ST_SEQ_TOO_LONG);
   const int slot = len - n + i;
   const bool rope = p.rope_cos != nullptr;
   const int page = p.page_table[static_cast<long long>(s) * p.max_pages + slot / kPage];
   const long long pos = static_cast<long long>(slot) + (p.pos_base != nullptr ? p.pos_base[b] : 0);
+  const bool far = rope && (pos < 0 || pos >= p.rope_rows);
+  float c[8] = {}, sn[8] = {};
+  if (rope && !far && h0 < p.Hq + p.Hkv) {
+    const float4 *pc = reinterpret_cast<const float4*>(p.rope_cos + pos * HALF + d),
+                 *ps = reinterpret_cast<const float4*>(p.rope_sin + pos * HALF + d);
+    *reinterpret_cast<float4*>(c) = pc[0];
+    *reinterpret_cast<float4*>(c + 4) = pc[1];
+    *reinterpret_cast<float4*>(sn) = ps[0];
+    *reinterpret_cast<float4*>(sn + 4) = ps[1];
+  }
   if (page < 0 || page >= p.n_pages) return flag(ST_BAD_PAGE);
-  if (rope && (pos < 0 || pos >= p.rope_rows)) return flag(ST_BAD_POS);
-
-  const S* src;
-  bool vec;
-  D* dst;
-  bool turn = rope;
-  if (h < p.Hq) {
-    src = static_cast<const S*>(p.q) + row * p.ld_q + h * DH;
-    vec = p.vec_q;
-    dst = static_cast<D*>(p.q_out) + (row * p.Hq + h) * DH;
-  } else {
-    const int hk = h - p.Hq;
-    const bool is_v = hk >= p.Hkv;
-    const int hh = is_v ? hk - p.Hkv : hk;
-    src = static_cast<const S*>(is_v ? p.v : p.k) + row * (is_v ? p.ld_v : p.ld_k) + hh * DH;
-    vec = is_v ? p.vec_v : p.vec_k;
-    dst = static_cast<D*>(is_v ? p.pool_v : p.pool_k) +
-          ((static_cast<long long>(page) * p.Hkv + hh) * kPage + slot % kPage) * DH;
-    turn = rope && !is_v;
-  }
-  float x1[8], x2[8];
-  load8<S>(src + d, vec, x1);
-  load8<S>(src + HALF + d, vec, x2);
-  if (turn) {
-    float c[8], sn[8];
-    load8<float>(p.rope_cos + pos * HALF + d, true, c);
-    load8<float>(p.rope_sin + pos * HALF + d, true, sn);
+  if (far) return flag(ST_BAD_POS);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float a = x1[k], e = x2[k];
-      x1[k] = a * c[k] - e * sn[k];
-      x2[k] = e * c[k] + a * sn[k];
+  for (int j = 0; j < kAppendHeads; ++j) {
+    const int h = h0 + j, hk = h - p.Hq;
+    if (h >= heads) break;
+    const bool is_v = hk >= p.Hkv;
+    float x1[8], x2[8];
+    raw[j][0].get(x1);
+    raw[j][1].get(x2);
+    if (rope && !is_v) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float a = x1[k], e = x2[k];
+        x1[k] = a * c[k] - e * sn[k];
+        x2[k] = e * c[k] + a * sn[k];
+      }
     }
+    D* dst = hk < 0 ? static_cast<D*>(p.q_out) + (row * p.Hq + h) * DH
+                    : static_cast<D*>(is_v ? p.pool_v : p.pool_k) +
+                          ((static_cast<long long>(page) * p.Hkv + (is_v ? hk - p.Hkv : hk)) * kPage + slot % kPage) * DH;
+    store8<D>(dst + d, x1);
+    store8<D>(dst + HALF + d, x2);
   }
-  store8<D>(dst + d, x1);
-  store8<D>(dst + HALF + d, x2);
 }
 
-template <typename S, typename D>
-cudaError_t launch_append_t(const AppendParams& p, int dh, unsigned blocks, cudaStream_t s) {
+template <typename S, typename D, bool VEC>
+cudaError_t launch_append_t(const AppendParams& p, int dh, cudaStream_t s) {
+  const long long units = (p.Hq + 2ll * p.Hkv + kAppendHeads - 1) / kAppendHeads;
+  const long long threads = static_cast<long long>(p.B) * p.T * units * (dh / 16);
+  const unsigned n = static_cast<unsigned>((threads + kAppendThreads - 1) / kAppendThreads);
   switch (dh) {
-    case 32: k_append<S, D, 32><<<blocks, kAppendThreads, 0, s>>>(p); break;
-    case 64: k_append<S, D, 64><<<blocks, kAppendThreads, 0, s>>>(p); break;
-    default: k_append<S, D, 128><<<blocks, kAppendThreads, 0, s>>>(p); break;
+    case 32: k_append<S, D, 32, VEC><<<n, kAppendThreads, 0, s>>>(p); break;
+    case 64: k_append<S, D, 64, VEC><<<n, kAppendThreads, 0, s>>>(p); break;
+    default: k_append<S, D, 128, VEC><<<n, kAppendThreads, 0, s>>>(p); break;
   }
   return cudaGetLastError();
 }
 
-template <typename S>
-cudaError_t launch_append_s(const AppendParams& p, int elem, int dh, unsigned blocks, cudaStream_t s) {
-  if (elem == DFLASH_ELEM_F32) return launch_append_t<S, float>(p, dh, blocks, s);
-  if (elem == DFLASH_ELEM_BF16) return launch_append_t<S, __nv_bfloat16>(p, dh, blocks, s);
-  return launch_append_t<S, __half>(p, dh, blocks, s);
+template <typename S, bool VEC>
+cudaError_t launch_append_s(const AppendParams& p, int elem, int dh, cudaStream_t s) {
+  if (elem == DFLASH_ELEM_F32) return launch_append_t<S, float, VEC>(p, dh, s);
+  if (elem == DFLASH_ELEM_BF16) return launch_append_t<S, __nv_bfloat16, VEC>(p, dh, s);
+  return launch_append_t<S, __half, VEC>(p, dh, s);
 }
 
 }  // namespace
@@ -221,21 +242,19 @@ dflash_status dflash_append_kv(const dflash_paged_kv* kv, const void* k, long lo
   p.n_pages = kv->n_pages;
   p.n_seqs = kv->n_seqs;
   p.max_pages = kv->max_pages;
-  p.vec_k = addr(k) % 16 == 0 && ld_k * size % 16 == 0;
-  p.vec_v = addr(v) % 16 == 0 && ld_v * size % 16 == 0;
-  p.vec_q = addr(q) % 16 == 0 && ld_q * size % 16 == 0;
   p.status = status;
-  const unsigned long long threads =
-      static_cast<unsigned long long>(B) * T * (Hq + 2ull * kv->n_kv_heads) * (dh / 16);
-  const unsigned long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
-  if (static_cast<long long>(B) * T > INT32_MAX || blocks > INT32_MAX) return DFLASH_ERR_UNSUPPORTED_SHAPE;
-  cudaError_t e;
-  if (src_elem == DFLASH_ELEM_F32)
-    e = launch_append_s<float>(p, kv->elem, dh, static_cast<unsigned>(blocks), stream);
-  else if (src_elem == DFLASH_ELEM_BF16)
-    e = launch_append_s<__nv_bfloat16>(p, kv->elem, dh, static_cast<unsigned>(blocks), stream);
-  else
-    e = launch_append_s<__half>(p, kv->elem, dh, static_cast<unsigned>(blocks), stream);
+  if (static_cast<long long>(B) * T > INT32_MAX ||
+      static_cast<unsigned long long>(B) * T * (Hq + 2ull * kv->n_kv_heads) * (dh / 16) / kAppendThreads > INT32_MAX)
+    return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  const auto aligned = [&](const void* a, long long ld) { return addr(a) % 16 == 0 && ld * size % 16 == 0; };
+  const bool vec = aligned(k, ld_k) && aligned(v, ld_v) && (q == nullptr || aligned(q, ld_q));
+  const auto run = [&](auto t) {
+    using S = decltype(t);
+    return vec ? launch_append_s<S, true>(p, kv->elem, dh, stream) : launch_append_s<S, false>(p, kv->elem, dh, stream);
+  };
+  const cudaError_t e = src_elem == DFLASH_ELEM_F32    ? run(float{})
+                        : src_elem == DFLASH_ELEM_BF16 ? run(__nv_bfloat16{})
+                                                       : run(__half{});
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
