@@ -266,15 +266,6 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c), "r"(h), "r"(page), "r"(smem_u32(bar))
       : "memory");
 }
-// One thread of a converged warp, the same one every time.  Copies and MMAs
-// take their operands from uniform registers: where the whole warp computes
-// them alike and one thread is elected to issue, they are there already.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
-  return is != 0;
-}
-
 // prefix_wide.cu: items of a tile of wide_rows(G) query rows (whole tokens),
 // n_prefix prefix items or n_own own ones.
 constexpr int kWideTile = 128;  // rows of an MMA
