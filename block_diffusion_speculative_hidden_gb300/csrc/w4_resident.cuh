@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   const int gr = lane >> 2, t4 = lane & 3;
   const bool elected = elect_one();
   uint64_t* full = reinterpret_cast<uint64_t*>(smem) + warp * kW4MaxStages;
+  uint64_t* x_full = reinterpret_cast<uint64_t*>(smem) + kW4Warps * kW4MaxStages;
   uint8_t* xs = smem + 1024;
   const uint32_t ring = smem_u32(smem) + (warp < p.low_warps ? p.off_ring + warp * p.stages * 2048
                                                              : p.off_high + (warp - p.low_warps) * p.stages * 2048);
@@ -79,11 +80,13 @@ __global__ void __launch_bounds__(kW4Threads, 1)
 
   if (lane == 0) {
     for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 33);  // (the TMA copy's arrival and the lanes')
+    mbar_init(&x_full[warp], 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   __syncwarp();
 
+  bool ok = true;
   // The warp's next unit to fetch.
   int f_chunk = -1, f_n = 0, f_at = 0, f_end = 0, f_tile = 0, f_unit = 0;
   auto f_settle = [&]() {  // on to the next chunk where this one's share is done
@@ -150,6 +153,17 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       f_settle();
     }
   };
+  // A chunk's activations: warps 0 .. M - 1 fetch a row each
+  auto fetch_x = [&](int c) {
+    const int k0 = c * p.chunk * kW4Unit, bytes = min(chunk_units(c) * kW4Unit, p.K - k0) * 2;
+    if (warp < p.M && elected) {
+      mbar_arrive_expect_tx(&x_full[warp], bytes);
+      bulk_load_global(smem_u32(xs) + warp * p.pitch, p.x + (static_cast<long long>(warp) * p.K + k0) / 8, bytes,
+                       &x_full[warp]);
+    }
+    __syncwarp();
+  };
+  fetch_x(0);
   int fetched = 0;
   for (; fetched < p.stages && f_chunk < p.chunks; ++fetched) fetch(fetched);
 
@@ -167,39 +181,31 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     asm("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(__byte_perm(w, lane4, 0x6504 | i << 4)));
     return v;
   };
-  // A chunk's activations: within a unit, thread t4's 8 k of word q at
-  // 64 q + 16 t4, as the pairs (k, k + 1) for E2M1, (k, k + 4) for integers
-  auto stage_x = [&](int c) {
-    const int n = chunk_units(c);
-    const int g = lane / (GROUP / 8), r = lane % (GROUP / 8);
-    const uint32_t d0 = smem_u32(xs) + (g * WPT + r % WPT) * 64 + r / WPT * 16;
-    // rows x units in turn, from another place in every CTA: otherwise all of
-    // them would ask the same few lines of the L2 at once
-    const int total = p.M * n, first = static_cast<int>((static_cast<long long>(total) * block) / gridDim.x);
-    auto each = [&](auto&& todo) {
-      int e = first + warp, m = e / n, u = e - m * n;
-      for (int i = warp; i < total; i += kW4Warps) {
-        if (m >= p.M) m -= p.M;
-        todo(m, u, d0 + m * p.pitch + u * 512);
-        for (u += kW4Warps; u >= n; u -= n) ++m;
-      }
-    };
-    each([&](int m, int u, uint32_t d) {
-      const int k = (c * p.chunk + u) * kW4Unit + lane * 8;
-      copy_async<16>(d, k < p.K ? p.x + (static_cast<long long>(m) * p.K + k) / 8 : p.x, k < p.K ? 16 : 0);
-    });
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if constexpr (!E2M1) {
-      each([&](int, int, uint32_t d) {
-        const uint4 v = lds128(d);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(__byte_perm(v.x, v.z, 0x5410)),
-                     "r"(__byte_perm(v.x, v.z, 0x7632)), "r"(__byte_perm(v.y, v.w, 0x5410)),
-                     "r"(__byte_perm(v.y, v.w, 0x7632))
-                     : "memory");
-      });
+  // All warps put the activations in place: within a unit, thread t4's 8 k of word q go
+  // to 64 q + 16 t4, as the pairs (k, k + 1) for E2M1, (k, k + 4) for integers
+  auto place_x = [&](int c) {
+    const int n = chunk_units(c), left = (p.K - c * p.chunk * kW4Unit) / 8 - lane;
+    const int g = lane / (GROUP / 8), r = lane % (GROUP / 8), to = (g * WPT + r % WPT) * 64 + r / WPT * 16;
+    const int parts = kW4Warps / p.M, part = warp / p.M, m = warp - part * p.M;
+    if (part >= parts) return;
+    ok = w4_wait(&x_full[m], c & 1, p.status) && ok;
+    __syncwarp();
+    const uint32_t row = smem_u32(xs) + m * p.pitch;
+#pragma unroll 4
+    for (int u = part; u < n; u += parts) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (u * 32 < left) v = lds128(row + u * 512 + lane * 16);
+      if constexpr (!E2M1)
+        v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                       __byte_perm(v.y, v.w, 0x7632));
+      __syncwarp();
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + u * 512 + to), "r"(v.x), "r"(v.y), "r"(v.z),
+                   "r"(v.w)
+                   : "memory");
     }
   };
-  stage_x(0);
+  __syncthreads();  // (the barriers of the activations are set up)
+  place_x(0);
   __syncthreads();  // the activations (and the table) are there
 
   // (rows past M are not kept: their columns of the sums are not either)
@@ -215,7 +221,6 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     woff[g] = gr * 128 + (((o >> 4) ^ gr) << 4) + (o & 15);
   }
 
-  bool ok = true;
   int s = 0;
   uint32_t parity = 0;
   for (int c = 0; c < p.chunks; ++c) {
@@ -367,11 +372,14 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       leave(tile);
     }
     if (c + 1 < p.chunks) {
-      stage_x(c + 1);
+      fence_proxy_async_smem();
+      fetch_x(c + 1);
+      place_x(c + 1);
       __syncthreads();
     }
   }
   if (!ok) {  // a wait gave up: copies still in flight get bounded waits before the CTA leaves
+    if (warp < p.M) w4_wait(&x_full[warp], (p.chunks - 1) & 1, p.status);
     for (int i = max(0, fetched - p.stages); i < fetched; ++i)
       w4_wait(&full[i % p.stages], static_cast<uint32_t>(i / p.stages) & 1, p.status);
   }
