@@ -536,6 +536,7 @@ constexpr int kWideFrom = 48;
 
 struct PrefixPlan {
   bool p_wide, s_wide;         // whether the wide kernel takes the prefix, the own parts (else the thin one)
+  bool pack;                   // prefix row tiles hold live rows only (where n_rows is given)
   bool merge, join;            // own parts add the prefix's partial results; a kernel joins them all
   long long p_tiles, s_tiles;  // row tiles of the wide kernel: of all groups (a bound), of an entry
   long long rows;
@@ -589,6 +590,12 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
   const int sms = plan_sms(), rows = wide_rows(std::min(G, kWideTile));
   if (r.p_wide) {
     r.p_tiles = (B * tg + static_cast<long long>(NG) * (rows - 1)) / rows;
+    // Packing the live rows takes a tile longer (3 us, and 4 percent of the loop)
+    // and pays where it saves CTAs a turn: 48 entries of 16 rows x 64 heads, a
+    // prefix of 8192, 160 us unpacked; packed 165 with all rows live, 96 with
+    // half of them.  In one turn (32 entries of 17 rows x 32 heads, 16384) the
+    // longest CTA stays as long: 134 us unpacked, packed 143 and 133.
+    r.pack = r.p_tiles * Hkv > 2ll * sms;
     // (beside the thin kernel, which waits for memory, one CTA an SM)
     r.p_chunks = plan_chunks(r.p_tiles * Hkv, mp, r.s_wide ? 2 * sms : sms, NG == 1, 0);
   }
@@ -657,23 +664,24 @@ bool page_map(const dflash_paged_kv& kv, void* base, int chunks, CUtensorMap* ou
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The queries as a 3-D map (elements, heads, tokens) with boxes of a row tile's
-// whole tokens x the group's heads x 64 elements.
-bool query_map(const dflash_paged_kv& kv, const void* q, int Hq, long long tokens, long long ld, CUtensorMap* out) {
+// The queries as a 3-D map (elements, heads, tokens) with boxes of 64 elements x
+// the group's heads x box_tokens.
+bool query_map(const dflash_paged_kv& kv, const void* q, int Hq, long long tokens, long long ld, int box_tokens,
+               CUtensorMap* out) {
   const auto fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   const int G = Hq / kv.n_kv_heads;
   const cuuint64_t gdim[3] = {static_cast<cuuint64_t>(kv.head_dim), static_cast<cuuint64_t>(Hq),
                               static_cast<cuuint64_t>(tokens)};
   const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(kv.head_dim) * 2, static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kWideTile / G)}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(box_tokens)}, es[3] = {1, 1, 1};
   return fn(out, kv.elem == DFLASH_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
             const_cast<void*>(q), gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct PrefixMaps {
-  CUtensorMap q, wide_k, wide_v, thin_k, thin_v;
+  CUtensorMap q, q_one, wide_k, wide_v, thin_k, thin_v;
 };
 
 template <typename T16, int DH, int NR>
@@ -694,9 +702,9 @@ template <typename T16, int DH>
 cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int elem, const PrefixMaps& m, cudaStream_t s) {
   const long long n_prefix = plan.p_tiles * plan.p_chunks * p.Hkv, n_own = p.B * plan.s_tiles * plan.s_chunks * p.Hkv;
   cudaError_t e = cudaSuccess;
-  if (plan.p_wide) e = launch_prefix_wide(p, elem, DH, n_prefix, 0, false, m.q, m.wide_k, m.wide_v, s);
+  if (plan.p_wide) e = launch_prefix_wide(p, elem, DH, n_prefix, 0, false, m.q, m.q_one, m.wide_k, m.wide_v, s);
   if (e == cudaSuccess)
-    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, 0, n_own, plan.p_wide, m.q, m.wide_k, m.wide_v, s)
+    e = plan.s_wide ? launch_prefix_wide(p, elem, DH, 0, n_own, plan.p_wide, m.q, m.q_one, m.wide_k, m.wide_v, s)
                     : plan.thin_rows == 8 ? launch_thin<T16, DH, 1>(p, plan.p_wide, m.thin_k, m.thin_v, s)
                             : launch_thin<T16, DH, 2>(p, plan.p_wide, m.thin_k, m.thin_v, s);
   if (e != cudaSuccess || !plan.join) return e;
@@ -756,11 +764,12 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   if (workspace_bytes < plan.bytes) return DFLASH_ERR_WORKSPACE;
   const long long ldq = one ? qd : ld_q;
   PrefixMaps maps{};
-  const int chunks = kv->head_dim / 64;
+  const int chunks = kv->head_dim / 64, G = n_q_heads / kv->n_kv_heads;
   if ((plan.warps > 0 && (!page_map(*kv, kv->k, chunks, &maps.thin_k) || !page_map(*kv, kv->v, chunks, &maps.thin_v))) ||
       ((plan.p_wide || plan.s_wide) &&
        (!page_map(*kv, kv->k, 1, &maps.wide_k) || !page_map(*kv, kv->v, 1, &maps.wide_v) ||
-        !query_map(*kv, q, n_q_heads, static_cast<long long>(B) * T, ldq, &maps.q))))
+        !query_map(*kv, q, n_q_heads, static_cast<long long>(B) * T, ldq, kWideTile / G, &maps.q) ||
+        !query_map(*kv, q, n_q_heads, static_cast<long long>(B) * T, ldq, 1, &maps.q_one))))
     return DFLASH_ERR_CUDA;
   PrefixParams p{};
   p.q = q;
@@ -785,6 +794,7 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.out = out;
   p.lse = lse;
   char* ws = static_cast<char*>(workspace);
+  p.pack = plan.pack && n_rows != nullptr;
   p.merge = plan.merge;
   p.p_thin = NG > 0 && !plan.p_wide;
   p.work = reinterpret_cast<long long*>(ws + plan.off_work);

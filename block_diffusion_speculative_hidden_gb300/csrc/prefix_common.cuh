@@ -26,6 +26,7 @@ struct PrefixParams {
   int p_tiles, p_chunks;  // prefix parts: row tiles over all groups (a bound), chunks of pages
   int s_tiles, s_chunks;  // own parts: row tiles of an entry, chunks of pages
   bool merge;             // own parts (of one chunk) add the prefix's partial results and write the result
+  bool pack;              // prefix row tiles of the wide kernel hold live rows only
   bool p_thin;            // the thin kernel takes the prefix parts (no p_chunks then)
   // what the thin kernel leaves for the joining one (ThinWork)
   long long* work;                // [NG] + [B] first pages, then pages a warp
@@ -271,7 +272,7 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, u
 constexpr int kWideTile = 128;  // rows of an MMA
 __host__ __device__ inline int wide_rows(int G) { return kWideTile / G * G; }
 cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, long long n_prefix, long long n_own,
-                               bool behind, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               bool behind, const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s);
 
 }  // namespace dflash

@@ -105,9 +105,111 @@ __device__ __forceinline__ constexpr uint32_t wide_idesc(int m, int n, bool b_mn
   return mma_idesc_f16_f32(m, n, b_mn) | (std::is_same<T16, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u);
 }
 
-template <typename T16, int DH>
+// A running sum over the CTA's threads: of v up to and including this thread's,
+// and (all) of every thread's.  warps: an int per warp in shared memory.
+template <int WARPS>
+__device__ __forceinline__ int cta_scan(int v, int* warps, int& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warps[warp] = v;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) v += warps[w];
+    all += warps[w];
+  }
+  __syncthreads();
+  return v;
+}
+
+// Prefix item `index` where entries have different numbers of rows: a group's
+// tiles take its live tokens one after the other, so that only a group's last
+// tile has rows without a query (a batch whose entries have 1 to 16 rows of 16
+// is half the work).  tokens[i]: the tile's i-th token (entry x T + row), or -1.  cum:
+// B + 1 ints.  The whole CTA asks.
+template <int WARPS>
+__device__ __noinline__ bool pack_item(const PrefixParams& p, int tile_tokens, Item* out, int* cum, int* warps, int* found,
+                                       int* tokens) {
+  int index = blockIdx.x;
+  Item it;
+  it.shared = true;
+  it.last = false;
+  it.chunk = index % p.p_chunks;
+  index /= p.p_chunks;
+  it.kvh = index % p.Hkv;
+  const int tile = index / p.Hkv;
+  // (a thread's first group is on the way while the entries are counted)
+  Group g{0, 0, -1, 0, 0, 0};
+  if (threadIdx.x < p.NG) g = load_group(p, threadIdx.x);
+  if (!bounds_ok(p)) return false;
+  int before = 0, all;
+  for (int e0 = 0; e0 < p.B; e0 += WARPS * 32) {
+    const int e = e0 + threadIdx.x, n = e < p.B ? entry_rows(p, e) : 0;
+    const int sum = cta_scan<WARPS>(n, warps, all);
+    if (e < p.B) cum[e + 1] = before + sum;
+    before += all;
+  }
+  if (threadIdx.x == 0) {
+    cum[0] = 0;
+    found[0] = -1;
+  }
+  __syncthreads();
+  before = 0;
+  for (int g0 = 0; g0 < p.NG; g0 += WARPS * 32) {
+    const int i = g0 + threadIdx.x;
+    if (g0 > 0 && i < p.NG) g = load_group(p, i);
+    int n = 0;
+    if (i < p.NG) {
+      n = (cum[g.hi] - cum[g.lo] + tile_tokens - 1) / tile_tokens;
+      if (blockIdx.x == 0) check_prefix(p, g.row);
+    }
+    const int sum = before + cta_scan<WARPS>(n, warps, all);
+    if (sum - n <= tile && tile < sum) {
+      found[0] = g.lo;
+      found[1] = g.hi;
+      found[2] = g.row;
+      found[3] = g.tokens;
+      found[4] = tile - (sum - n);
+    }
+    before += all;
+  }
+  __syncthreads();
+  if (found[0] < 0) return false;
+  g = Group{found[0], found[1], found[2], found[3], found[4], 0};
+  const int first = cum[g.lo] + g.tile * tile_tokens;
+  it.b0 = g.lo;
+  it.row0 = g.tile * tile_tokens * p.G;
+  it.rows = (cum[g.hi] - cum[g.lo]) * p.G;
+  it.tokens = g.tokens;
+  it.table_row = g.row;
+  const int pages = pages_of(it.tokens), per = chunk_pages(pages, p.p_chunks);
+  it.pg0 = it.chunk * per;
+  it.pg1 = min(pages, it.pg0 + per);
+  if (it.pg0 >= it.pg1) return false;
+  for (int i = threadIdx.x; i < tile_tokens; i += WARPS * 32) {
+    int lo = g.lo, hi = g.hi - 1;  // the last entry of those that begin no later
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cum[mid] <= first + i) lo = mid;
+      else hi = mid - 1;
+    }
+    tokens[i] = first + i < cum[g.hi] ? lo * p.T + first + i - cum[lo] : -1;
+  }
+  if (threadIdx.x == 0) *out = it;
+  __syncthreads();
+  return true;
+}
+
+// PACK: prefix items of entries with different numbers of rows (pack_item).
+template <typename T16, int DH, bool PACK>
 __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
-    k_prefix_wide(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+    k_prefix_wide(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+                  const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p, int n_prefix) {
   using L = WideLayout<DH>;
   using M16 = Mma16<T16>;
@@ -130,7 +232,29 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
   pdl_trigger();  // (the kernels behind wait for this one's results on their own)
   const int rows_tile = wide_rows(p.G);
   Item it;
-  if (!find_item(p, blockIdx.x, n_prefix, rows_tile, it)) return pdl_wait();
+  int* tokens = reinterpret_cast<int*>(red);  // (PACK; until the softmax begins its place is free)
+  if constexpr (PACK) {
+    Item* found = reinterpret_cast<Item*>(tokens + kWideTile + 64);
+    if (!pack_item<L::THREADS / 32>(p, rows_tile / p.G, found, reinterpret_cast<int*>(smem + L::OFF_KV),
+                                    tokens + kWideTile, tokens + kWideTile + 32, tokens))
+      return pdl_wait();
+    // (known to be alike in a warp, these are kept in the uniform registers: else
+    // the softmax loop, short of registers, is 5 to 10 percent slower)
+    const auto alike = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    it.shared = true;
+    it.last = false;
+    it.b0 = alike(found->b0);
+    it.row0 = alike(found->row0);
+    it.rows = alike(found->rows);
+    it.kvh = alike(found->kvh);
+    it.chunk = alike(found->chunk);
+    it.tokens = alike(found->tokens);
+    it.table_row = alike(found->table_row);
+    it.pg0 = alike(found->pg0);
+    it.pg1 = alike(found->pg1);
+  } else if (!find_item(p, blockIdx.x, n_prefix, rows_tile, it)) {
+    return pdl_wait();
+  }
   const int np = max(0, it.pg1 - it.pg0);
   const int n = (np + kWidePages - 1) / kWidePages;  // key tiles
 
@@ -147,6 +271,14 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     mbar_init(part_full, kWideTile);
     fence_mbar_init();
     fence_proxy_async_smem();
+  }
+  if (PACK && threadIdx.x < kWideTile) {  // rows without a query: zeros
+    const int r = threadIdx.x;
+    if (r >= rows_tile || tokens[r / p.G] < 0) {
+      for (int z = 0; z < L::NCH * 8; ++z)
+        *reinterpret_cast<uint4*>(smem + z / 8 * L::Q_CH + r * 128 + z % 8 * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, L::COLS);
@@ -178,7 +310,25 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
       };
       int ids = page_ids(0), next = page_ids(32), issued = 0;
       bool ok = true;
-      if (elected && key_tiles > 0) {
+      if constexpr (PACK) {  // the tile's tokens, a copy each
+        const int live = __shfl_sync(0xffffffffu, min(rows_tile, it.rows - it.row0), 0) / p.G;
+        if (elected) mbar_arrive_expect_tx(q_full, live * p.G * L::NCH * 128);
+        const int begin = __shfl_sync(0xffffffffu, tokens[0], 0);
+        const bool run = live * p.G == rows_tile && __shfl_sync(0xffffffffu, tokens[live - 1], 0) == begin + live - 1;
+        if (run && elected) {  // (of entries with all their rows)
+#pragma unroll
+          for (int cc = 0; cc < L::NCH; ++cc)
+            tma_rows(smem_u32(smem) + cc * L::Q_CH, &tmQ, q_full, cc * 64, kvh * p.G, begin);
+        }
+        for (int t = run ? live : 0; t < live; ++t) {
+          const int token = __shfl_sync(0xffffffffu, tokens[t], 0);
+          if (elected) {
+#pragma unroll
+            for (int cc = 0; cc < L::NCH; ++cc)
+              tma_rows(smem_u32(smem) + cc * L::Q_CH + t * p.G * 128, &tmQ1, q_full, cc * 64, kvh * p.G, token);
+          }
+        }
+      } else if (elected && key_tiles > 0) {
         // whole tokens: a tile's first row is a token's first head of the group
         mbar_arrive_expect_tx(q_full, rows_tile * L::NCH * 128);
         for (int cc = 0; cc < L::NCH; ++cc)
@@ -278,9 +428,17 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     // ---------------- softmax: threads r of the two halves own row r
     const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
     const int pair = 1 + quad;  // the named barrier of the row's two warps
-    Row row = find_row(p, it, it.row0 + r);
-    row.live = row.live && r < rows_tile;
-    const int parts = it.last && p.merge ? chunks_of(pages_of(group_of(p, it.b0).tokens), p.p_chunks) : 0;  // of the prefix, to be added at the end
+    int at, seen;  // the row's place in the output (-1: none; below 2^30) and the keys that it sees
+    if constexpr (PACK) {
+      const int token = r < rows_tile ? tokens[r / p.G] : -1;
+      at = token < 0 ? -1 : token * p.Hq + it.kvh * p.G + r % p.G;
+      seen = it.tokens;
+    } else {
+      const Row row = find_row(p, it, it.row0 + r);
+      at = row.live && r < rows_tile ? static_cast<int>(row.at) : -1;
+      seen = row.seen;
+    }
+    const int parts = !PACK && it.last && p.merge ? chunks_of(pages_of(group_of(p, it.b0).tokens), p.p_chunks) : 0;  // of the prefix, to be added at the end
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_at = tmem + lanes + L::S_COL + 64 * half, p_at = tmem + lanes + L::P_COL + 4 * L::P_PAGE * half;
     const uint32_t o_at = tmem + lanes + L::O_COL + DH / 2 * half;
@@ -311,7 +469,7 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
         tc_fence_after();
       }
       // keys of this half that the row sees (the chunk may end inside the tile)
-      const int lim = min(row.seen, it.pg1 * kPage) - key0 - 64 * half;
+      const int lim = min(seen, it.pg1 * kPage) - key0 - 64 * half;
       if (__any_sync(0xffffffffu, lim < 64)) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
@@ -427,14 +585,14 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
       float weight = 1.f;
       for (int c = 0; c < parts; ++c) {
         if (half == 0) {
-          if (row.live) {
+          if (at >= 0) {
             mbar_arrive_expect_tx(part_full, DH * 4);
-            bulk_load_global(smem_u32(stage), p.part_o + (c * R + row.at) * DH, DH * 4, part_full);
+            bulk_load_global(smem_u32(stage), p.part_o + (c * R + at) * DH, DH * 4, part_full);
           } else {
             mbarrier_arrive_one(part_full);
           }
         }
-        const float other = row.live ? p.part_lse[c * R + row.at] : -INFINITY;
+        const float other = at >= 0 ? p.part_lse[c * R + at] : -INFINITY;
         const float top = fmaxf(lse2, other), base = top == -INFINITY ? 0.f : top;
         const float f0 = wide_ex2(lse2 - base), f1 = wide_ex2(other - base);
         ok = ok && mbar_wait(part_full, c & 1, p.status);
@@ -470,11 +628,11 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     }
     fence_proxy_async_smem();
     wide_bar(pair, 64);
-    if (row.live && half == 0) {
-      const long long part = (it.shared ? it.chunk : p.p_chunks + it.chunk) * R + row.at;
+    if (at >= 0 && half == 0) {
+      const long long part = (it.shared ? it.chunk : p.p_chunks + it.chunk) * R + at;
       if (it.last) {
-        bulk_store_row(static_cast<T16*>(p.out) + row.at * DH, smem_u32(stage), DH * 2);
-        if (p.lse != nullptr) p.lse[row.at] = lse2 * 0.69314718055994531f;
+        bulk_store_row(static_cast<T16*>(p.out) + at * DH, smem_u32(stage), DH * 2);
+        if (p.lse != nullptr) p.lse[at] = lse2 * 0.69314718055994531f;
       } else {
         bulk_store_row(p.part_o + part * DH, smem_u32(stage), DH * 4);
         p.part_lse[part] = lse2;
@@ -492,29 +650,34 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
   pdl_wait();  // (the joining kernel behind starts once all of this one has left)
 }
 
-template <typename T16, int DH>
+template <typename T16, int DH, bool PACK>
 cudaError_t launch_wide_t(const PrefixParams& p, long long n_prefix, long long n_own, bool behind,
-                          const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+                          const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   using L = WideLayout<DH>;
   static FuncAttr attr;
   const cudaError_t e = attr.ensure(L::SMEM, [](int v) {
-    return cudaFuncSetAttribute(k_prefix_wide<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+    return cudaFuncSetAttribute(k_prefix_wide<T16, DH, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
   });
   if (e != cudaSuccess) return e;
-  return launch_k(k_prefix_wide<T16, DH>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(L::THREADS), L::SMEM, s,
-                  dim3(1), behind, tq, tk, tv, p, static_cast<int>(n_prefix));
+  return launch_k(k_prefix_wide<T16, DH, PACK>, dim3(static_cast<unsigned>(n_prefix + n_own)), dim3(L::THREADS), L::SMEM, s,
+                  dim3(1), behind, tq, tq1, tk, tv, p, static_cast<int>(n_prefix));
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_wide(const PrefixParams& p, int elem, int head_dim, long long n_prefix, long long n_own,
-                               bool behind, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               bool behind, const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s) {
+  const auto run = [&](auto t, auto pack) {
+    using T16 = decltype(t);
+    constexpr bool PACK = decltype(pack)::value;
+    return head_dim == 64 ? launch_wide_t<T16, 64, PACK>(p, n_prefix, n_own, behind, tq, tq1, tk, tv, s)
+                          : launch_wide_t<T16, 128, PACK>(p, n_prefix, n_own, behind, tq, tq1, tk, tv, s);
+  };
+  const bool pack = n_own == 0 && p.pack;
   if (elem == DFLASH_ELEM_BF16)
-    return head_dim == 64 ? launch_wide_t<__nv_bfloat16, 64>(p, n_prefix, n_own, behind, tq, tk, tv, s)
-                          : launch_wide_t<__nv_bfloat16, 128>(p, n_prefix, n_own, behind, tq, tk, tv, s);
-  return head_dim == 64 ? launch_wide_t<__half, 64>(p, n_prefix, n_own, behind, tq, tk, tv, s)
-                        : launch_wide_t<__half, 128>(p, n_prefix, n_own, behind, tq, tk, tv, s);
+    return pack ? run(__nv_bfloat16{}, std::true_type{}) : run(__nv_bfloat16{}, std::false_type{});
+  return pack ? run(__half{}, std::true_type{}) : run(__half{}, std::false_type{});
 }
 
 }  // namespace dflash
