@@ -34,8 +34,9 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 
 constexpr int kThinWarps = 4;
 constexpr int kThinThreads = kThinWarps * 32;
+constexpr int kThinRows = 8;    // query rows of a tile (a multiple of the 8 columns of an MMA)
 constexpr int kThinStages = 3;  // pages in flight per warp
-constexpr int kThinPages = 2;   // pages that a warp takes at least
+constexpr int kThinPages = 1;   // pages that a warp takes at least (one sequence of 577 tokens: 1 7.4 us, 2 9.9, 4 10.9)
 constexpr int kMaxEntries = 4096;  // batch entries, and groups, of a call
 
 template <int DH>
@@ -107,7 +108,7 @@ __device__ __forceinline__ void thin_line(const PrefixParams& p, int groups, boo
     if (e < n && (e >= groups || ok)) {
       const ThinPart t = thin_read(p, groups, e);
       if (held != nullptr) held[e] = make_int4(t.b0, t.rows, t.tokens, t.table_row);
-      size = static_cast<long long>(thin_tiles(t.rows, p.thin_rows)) * p.Hkv * pages_of(t.tokens);
+      size = static_cast<long long>(thin_tiles(t.rows, kThinRows)) * p.Hkv * pages_of(t.tokens);
       if (check) {
         if (t.shared) check_prefix(p, t.table_row);
         else check_entry(p, t.b0, t.table_row);
@@ -171,14 +172,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // Independent warps, each with a ring of pages that runs on over the parts it
 // takes, and its own running maxima, sums and outputs.  The products are taken
 // transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and dimensions fill
-// the 16 rows of an MMA and the few query rows its 8 columns (NR of them).
-template <typename T16, int DH, int NR>
+// the 16 rows of an MMA and the query rows its 8 columns.
+template <typename T16, int DH>
 __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
                                                               const __grid_constant__ PrefixParams p) {
   using L = ThinLayout<DH>;
   using M = Mma16<T16>;
-  constexpr int KS = DH / 16;
+  constexpr int KS = DH / 16, NR = kThinRows / 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   long long* first = reinterpret_cast<long long*>(smem + L::BYTES);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     it.rows = part.rows;
     it.tokens = part.tokens;
     it.kvh = unit % p.Hkv;
-    it.row0 = unit / p.Hkv * (8 * NR);
+    it.row0 = unit / p.Hkv * kThinRows;
 
     // query row 8j + gr as a B fragment
     uint32_t qf[NR][KS][2];
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
         const int r = 8 * j + 2 * t4 + h;
         const Row row = find_row(p, it, it.row0 + r);
         if (!row.live) continue;
-        const long long at = all ? (it.shared ? 0 : R) + row.at : static_cast<long long>(slot) * p.thin_rows + r;
+        const long long at = all ? (it.shared ? 0 : R) + row.at : static_cast<long long>(slot) * kThinRows + r;
         const float inv = l[j][h] > 0.f ? 1.f / l[j][h] : 0.f;
         float* dst = (all ? p.whole_o : p.slot_o) + at * DH + gr;
 #pragma unroll
@@ -427,9 +428,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
     if (p.s_chunks > 0) n[1] = chunks_of(own, p.s_chunks);
     if (p.warps > 0) per = thin_per(first[groups + p.B], p.warps);
     auto on_line = [&](int which, int e, int pages, int r) {
-      f0[which] = first[e] + static_cast<long long>(r / p.thin_rows * p.Hkv + kvh) * pages;
+      f0[which] = first[e] + static_cast<long long>(r / kThinRows * p.Hkv + kvh) * pages;
       w0[which] = thin_div(f0[which], per);
-      lane_row[which] = r % p.thin_rows;
+      lane_row[which] = r % kThinRows;
       n[which] = pages > 0 ? static_cast<int>(thin_div(f0[which] + pages - 1, per) - w0[which]) + 1 : 0;
     };
     const int gi = h - kvh * p.G;
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
       o = p.whole_o;
     } else {
       const long long w = w0[which] + k;
-      at = (2 * w + (k > 0 || f0[which] == w * per ? 0 : 1)) * p.thin_rows + lane_row[which];
+      at = (2 * w + (k > 0 || f0[which] == w * per ? 0 : 1)) * kThinRows + lane_row[which];
       lse = p.slot_lse;
       o = p.slot_o;
     }
@@ -530,9 +531,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 
 // ------------------------------------------------------------------ host side
 
-// From this many query rows (of an entry; of a group on average) on, the
-// wide kernel takes them.
-constexpr int kWideFrom = 48;
+// From this many query rows (of an entry; of a group on average) on, the wide
+// kernel takes them: where a second thin tile would read the keys again.
+// Thin / wide, heads of 128 with 4 (8) query heads a kv head, 64 sequences of
+// 1024 tokens: 4 rows 51 / 53 us, 8 rows 56 / 54, 16 rows 71 / 55; two
+// sequences of 300: 4 rows 7.5 / 10.1, 8 rows 7.7 / 10.2, 16 rows 11.3 / 10.5;
+// a prefix of 131000: 8 rows 91 / 89, 16 rows 148 / 90.
+constexpr int kWideFrom = 9;
 
 struct PrefixPlan {
   bool p_wide, s_wide;         // whether the wide kernel takes the prefix, the own parts (else the thin one)
@@ -541,7 +546,7 @@ struct PrefixPlan {
   long long p_tiles, s_tiles;  // row tiles of the wide kernel: of all groups (a bound), of an entry
   long long rows;
   int p_chunks, s_chunks;      // of the wide kernel's parts (0: the thin kernel's)
-  int warps, thin_rows;        // of the thin kernel (0: not used): warps, and query rows of a tile (8 or 16)
+  int warps;                   // of the thin kernel (0: not used)
   size_t off_work, off_lse, off_o, off_whole_lse, off_whole_o, off_slot_lse, off_slot_o, bytes;
 };
 
@@ -596,8 +601,10 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
     // half of them.  In one turn (32 entries of 17 rows x 32 heads, 16384) the
     // longest CTA stays as long: 134 us unpacked, packed 143 and 133.
     r.pack = r.p_tiles * Hkv > 2ll * sms;
-    // (beside the thin kernel, which waits for memory, one CTA an SM)
-    r.p_chunks = plan_chunks(r.p_tiles * Hkv, mp, r.s_wide ? 2 * sms : sms, NG == 1, 0);
+    // Beside a thin kernel that reads as much (it waits for memory) one CTA an
+    // SM, else two: 4 sequences of 300 tokens behind 131000, 118 and 93 us.
+    const bool beside = !r.s_wide && static_cast<long long>(B) * ml >= static_cast<long long>(NG) * mp;
+    r.p_chunks = plan_chunks(r.p_tiles * Hkv, mp, beside ? sms : 2 * sms, NG == 1, 0);
   }
   if (r.s_wide) {
     r.s_tiles = (tg + rows - 1) / rows;
@@ -607,8 +614,7 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
     r.join = r.s_chunks > 1 || (NG > 0 && !r.merge);
   } else {
     // as many warps as the SMs hold, or as there can be shares of kThinPages pages
-    r.thin_rows = tg <= 8 && (NG == 0 || r.p_wide || B * tg <= 8 * static_cast<long long>(NG)) ? 8 : 16;
-    const auto tiles = [&](long long n) { return (n + r.thin_rows - 1) / r.thin_rows; };
+    const auto tiles = [](long long n) { return (n + kThinRows - 1) / kThinRows; };
     const long long line = B * tiles(tg) * Hkv * ((ml + kPage - 1) / kPage) +
                            (NG > 0 && !r.p_wide ? (tiles(B * tg) + NG) * Hkv * ((mp + kPage - 1) / kPage) : 0);
     // (beside the wide kernel's CTAs half of them: all of a line's warps start at once)
@@ -619,7 +625,7 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
   }
   if (r.p_tiles * Hkv * r.p_chunks > INT32_MAX || B * r.s_tiles * Hkv * r.s_chunks > INT32_MAX) return false;
   const size_t parts = r.join || r.merge ? r.p_chunks + (r.join ? r.s_chunks : 0) : 0;
-  const size_t dh = kv.head_dim, whole = r.warps > 0 ? 2 * r.rows : 0, slots = 2ull * r.warps * r.thin_rows;
+  const size_t dh = kv.head_dim, whole = r.warps > 0 ? 2 * r.rows : 0, slots = 2ull * r.warps * kThinRows;
   size_t off = 256;  // (the first 256 bytes: a status word for callers without one)
   const auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -684,17 +690,17 @@ struct PrefixMaps {
   CUtensorMap q, q_one, wide_k, wide_v, thin_k, thin_v;
 };
 
-template <typename T16, int DH, int NR>
+template <typename T16, int DH>
 cudaError_t launch_thin(const PrefixParams& p, bool behind, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t s) {
   const int line = (p.p_thin ? p.NG : 0) + p.B;
   const int smem = ThinLayout<DH>::SMEM + (line + 2) / 2 * 16 + (line <= kThinHeld ? line * 16 : 0);
   static FuncAttr attr;
   const cudaError_t e = attr.ensure(smem, [](int v) {
-    return cudaFuncSetAttribute(k_prefix_thin<T16, DH, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+    return cudaFuncSetAttribute(k_prefix_thin<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
   });
   if (e != cudaSuccess) return e;
-  return launch_k(k_prefix_thin<T16, DH, NR>, dim3(p.warps / kThinWarps), dim3(kThinThreads), smem, s, dim3(1), behind,
+  return launch_k(k_prefix_thin<T16, DH>, dim3(p.warps / kThinWarps), dim3(kThinThreads), smem, s, dim3(1), behind,
                   tk, tv, p);
 }
 
@@ -705,8 +711,7 @@ cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int ele
   if (plan.p_wide) e = launch_prefix_wide(p, elem, DH, n_prefix, 0, false, m.q, m.q_one, m.wide_k, m.wide_v, s);
   if (e == cudaSuccess)
     e = plan.s_wide ? launch_prefix_wide(p, elem, DH, 0, n_own, plan.p_wide, m.q, m.q_one, m.wide_k, m.wide_v, s)
-                    : plan.thin_rows == 8 ? launch_thin<T16, DH, 1>(p, plan.p_wide, m.thin_k, m.thin_v, s)
-                            : launch_thin<T16, DH, 2>(p, plan.p_wide, m.thin_k, m.thin_v, s);
+                    : launch_thin<T16, DH>(p, plan.p_wide, m.thin_k, m.thin_v, s);
   if (e != cudaSuccess || !plan.join) return e;
   // few rows: a row's parts over all the warps of a CTA
   const int share = plan.rows < 8ll * 152 ? kJoinWarps : 1, per = kJoinWarps / share;
@@ -805,7 +810,6 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
   p.slot_lse = reinterpret_cast<float*>(ws + plan.off_slot_lse);
   p.slot_o = reinterpret_cast<float*>(ws + plan.off_slot_o);
   p.warps = plan.warps;
-  p.thin_rows = plan.thin_rows;
   p.status = status != nullptr ? status : reinterpret_cast<int*>(ws);
   p.p_tiles = static_cast<int>(plan.p_tiles);
   p.p_chunks = plan.p_chunks;

@@ -28,11 +28,11 @@ struct PrefixParams {
   bool merge;             // own parts (of one chunk) add the prefix's partial results and write the result
   bool pack;              // prefix row tiles of the wide kernel hold live rows only
   bool p_thin;            // the thin kernel takes the prefix parts (no p_chunks then)
-  // what the thin kernel leaves for the joining one (ThinWork)
-  long long* work;                // [NG] + [B] first pages, then pages a warp
+  // what the thin kernel leaves for the joining one
+  long long* work;                // the line's first pages of [NG] + [B] elements, and its length
   float *whole_lse, *whole_o;     // [2][B*T*Hq], [..][DH]: prefix and own parts that one warp took whole
-  float *slot_lse, *slot_o;       // [2 * warps][thin_rows], [..][DH]: a warp's first and last part, where others share them
-  int warps, thin_rows;           // its warps, and the query rows of its tiles
+  float *slot_lse, *slot_o;       // [2 * warps][rows of a tile], [..][DH]: a warp's first and last part, where others share them
+  int warps;                      // its warps
 };
 
 // Chunks are whole multiples of this many pages (a key tile of the wide
