@@ -32,21 +32,23 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-constexpr int kThinWarps = 4;
-constexpr int kThinThreads = kThinWarps * 32;
 constexpr int kThinRows = 8;    // query rows of a tile (a multiple of the 8 columns of an MMA)
-constexpr int kThinStages = 3;  // pages in flight per warp
 constexpr int kThinPages = 1;   // pages that a warp takes at least (one sequence of 577 tokens: 1 7.4 us, 2 9.9, 4 10.9)
 constexpr int kMaxEntries = 4096;  // batch entries, and groups, of a call
 
 template <int DH>
 struct ThinLayout {
+  // Warps and pages in flight a warp.  Heads of 128 (64): 64 sequences of up to
+  // 1500 tokens beside a shared prefix, 4 warps x 3 pages 68 us, 6 x 2 58; 64
+  // sequences of 1024 (64 query heads of 64), 33 and 37.
+  static constexpr int WARPS = DH == 64 ? 4 : 6, THREADS = WARPS * 32, STAGES = DH == 64 ? 3 : 2;
+  static constexpr int CTAS = DH == 64 ? 4 : 2;           // that an SM holds
   static constexpr int HALF_PAGE = kPage * DH * 2;        // bytes of a page of K (or V) of one head
   static constexpr int STAGE = 2 * HALF_PAGE;
-  static constexpr int WARP = kThinStages * STAGE;
-  static constexpr int OFF_SCAN = kThinWarps * WARP;
+  static constexpr int WARP = STAGES * STAGE;
+  static constexpr int OFF_SCAN = WARPS * WARP;
   static constexpr int OFF_BAR = OFF_SCAN + 64;
-  static constexpr int BYTES = OFF_BAR + kThinWarps * kThinStages * 8;
+  static constexpr int BYTES = OFF_BAR + WARPS * STAGES * 8;
   static constexpr int SMEM = 1024 + BYTES;               // + the line: first pages of its elements, their rows and pages
   static_assert(BYTES % 16 == 0, "the line is aligned");
 };
@@ -174,7 +176,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and dimensions fill
 // the 16 rows of an MMA and the query rows its 8 columns.
 template <typename T16, int DH>
-__global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(ThinLayout<DH>::THREADS) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
                                                               const __grid_constant__ PrefixParams p) {
   using L = ThinLayout<DH>;
@@ -190,19 +192,19 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
   const int groups = p.p_thin ? p.NG : 0, n_line = groups + p.B;
   const bool sound = p.NG == 0 || bounds_ok(p);
   if (blockIdx.x == 0 && threadIdx.x == 0 && !sound) flag_status(p.status, ST_BAD_BLOCK);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * kThinStages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR) + warp * L::STAGES;
   if (lane == 0) {
-    for (int s = 0; s < kThinStages; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < L::STAGES; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  thin_line<kThinWarps>(p, groups, sound, blockIdx.x == 0, first, n_line <= kThinHeld ? thin_held(first, n_line) : nullptr,
+  thin_line<L::WARPS>(p, groups, sound, blockIdx.x == 0, first, n_line <= kThinHeld ? thin_held(first, n_line) : nullptr,
                         reinterpret_cast<long long*>(smem + L::OFF_SCAN));
   const long long length = first[n_line], per = thin_per(length, p.warps);
   if (blockIdx.x == 0 && n_line > kThinHeld) {  // (a shorter line the joining kernel sets up itself)
-    for (int e = threadIdx.x; e <= n_line; e += kThinThreads) p.work[e] = first[e];
+    for (int e = threadIdx.x; e <= n_line; e += L::THREADS) p.work[e] = first[e];
   }
-  const int self = blockIdx.x * kThinWarps + warp;
+  const int self = blockIdx.x * L::WARPS + warp;
   const long long f0 = self * per, f1 = min(length, f0 + per);
   const int mine = f1 > f0 ? static_cast<int>(f1 - f0) : 0;
   uint8_t* ring = smem + warp * L::WARP;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
   auto issue = [&](int i) {
     if (i > 0 && (i & 31) == 0) fetch_ids(i);
     const int id = __shfl_sync(0xffffffffu, ids, i & 31), head = __shfl_sync(0xffffffffu, heads, i & 31);
-    const int s = i % kThinStages;
+    const int s = i % L::STAGES;
     const uint32_t kd = smem_u32(smem) + warp * L::WARP + s * L::STAGE;
     if (elected) {
       mbar_arrive_expect_tx(&bars[s], L::STAGE);
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
       }
     }
     if (i == 0) {  // (the pages' first copies, behind the loads of the first queries)
-      for (int c = 0; c < min(mine, kThinStages); ++c) issue(c);
+      for (int c = 0; c < min(mine, L::STAGES); ++c) issue(c);
     }
     // rows 8j + 2 t4 and the next one are this thread's in S^T and O^T
     int seen[NR][2];
@@ -290,8 +292,8 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
     for (int j = 0; j < NR; ++j) m[j][0] = m[j][1] = -INFINITY;
 
     for (int c = 0; c < share; ++c, ++i) {
-      const int s = i % kThinStages;
-      ok = ok && mbar_wait(&bars[s], (i / kThinStages) & 1, p.status);
+      const int s = i % L::STAGES;
+      ok = ok && mbar_wait(&bars[s], (i / L::STAGES) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok) != 0;
       if (!ok) break;
       const int key0 = (pg0 + c) * kPage;
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
         for (int j = 0; j < NR; ++j) M::mma(o[j][d], va, pb[j][0], pb[j][1]);
       }
       __syncwarp();
-      if (i + kThinStages < mine) issue(i + kThinStages);
+      if (i + L::STAGES < mine) issue(i + L::STAGES);
     }
 
     // the share's result, normalised by its own sum
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThinThreads) k_prefix_thin(const __grid_const
       }
   }
   if (!ok) {  // a wait gave up: what is still in flight gets its own bounded waits before the CTA leaves
-    for (int c = i; c < min(mine, i + kThinStages); ++c) mbar_wait(&bars[c % kThinStages], (c / kThinStages) & 1, p.status);
+    for (int c = i; c < min(mine, i + L::STAGES); ++c) mbar_wait(&bars[c % L::STAGES], (c / L::STAGES) & 1, p.status);
   }
   pdl_wait();  // (the joining kernel starts its work once all of this one has left, and what ran before it)
 }
@@ -618,9 +620,12 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
     const long long line = B * tiles(tg) * Hkv * ((ml + kPage - 1) / kPage) +
                            (NG > 0 && !r.p_wide ? (tiles(B * tg) + NG) * Hkv * ((mp + kPage - 1) / kPage) : 0);
     // (beside the wide kernel's CTAs half of them: all of a line's warps start at once)
-    const long long most = static_cast<long long>(sms) * (kv.head_dim == 64 ? 4 : 2) / (r.p_wide ? 2 : 1) * kThinWarps;
+    const bool d64 = kv.head_dim == 64;
+    const int per_cta = d64 ? ThinLayout<64>::WARPS : ThinLayout<128>::WARPS;
+    const int ctas = d64 ? ThinLayout<64>::CTAS : ThinLayout<128>::CTAS;
+    const long long most = static_cast<long long>(sms) * ctas / (r.p_wide ? 2 : 1) * per_cta;
     const long long want = (line + kThinPages - 1) / kThinPages;
-    r.warps = static_cast<int>(std::min(most, (want + kThinWarps - 1) / kThinWarps * kThinWarps));
+    r.warps = static_cast<int>(std::min(most, (want + per_cta - 1) / per_cta * per_cta));
     r.join = true;
   }
   if (r.p_tiles * Hkv * r.p_chunks > INT32_MAX || B * r.s_tiles * Hkv * r.s_chunks > INT32_MAX) return false;
@@ -700,7 +705,7 @@ cudaError_t launch_thin(const PrefixParams& p, bool behind, const CUtensorMap& t
     return cudaFuncSetAttribute(k_prefix_thin<T16, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
   });
   if (e != cudaSuccess) return e;
-  return launch_k(k_prefix_thin<T16, DH>, dim3(p.warps / kThinWarps), dim3(kThinThreads), smem, s, dim3(1), behind,
+  return launch_k(k_prefix_thin<T16, DH>, dim3(p.warps / ThinLayout<DH>::WARPS), dim3(ThinLayout<DH>::THREADS), smem, s, dim3(1), behind,
                   tk, tv, p);
 }
 
