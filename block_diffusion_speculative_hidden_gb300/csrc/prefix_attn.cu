@@ -373,14 +373,14 @@ __global__ void __launch_bounds__(ThinLayout<DH>::THREADS) k_prefix_thin(const _
         const Row row = find_row(p, it, it.row0 + r);
         if (!row.live) continue;
         const long long at = all ? (it.shared ? 0 : R) + row.at : static_cast<long long>(slot) * kThinRows + r;
-        const float inv = l[j][h] > 0.f ? 1.f / l[j][h] : 0.f;
+        const float inv = l[j][h] != 0.f ? 1.f / l[j][h] : 0.f;
         float* dst = (all ? p.whole_o : p.slot_o) + at * DH + gr;
 #pragma unroll
         for (int d = 0; d < KS; ++d) {
           dst[16 * d] = o[j][d][h] * inv;
           dst[16 * d + 8] = o[j][d][2 + h] * inv;
         }
-        if (gr == 0) (all ? p.whole_lse : p.slot_lse)[at] = l[j][h] > 0.f ? m[j][h] + log2f(l[j][h]) : -INFINITY;
+        if (gr == 0) (all ? p.whole_lse : p.slot_lse)[at] = l[j][h] != 0.f ? m[j][h] + log2f(l[j][h]) : -INFINITY;
       }
   }
   if (!ok) {  // a wait gave up: what is still in flight gets its own bounded waits before the CTA leaves
@@ -524,11 +524,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
   }
   const float ms = mx == -INFINITY ? 0.f : mx;
   if (!live) return;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   T16* dst = static_cast<T16*>(p.out) + row * DH + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = M::pack(a[e] * inv, a[e + 1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum > 0.f ? (ms + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum != 0.f ? (ms + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host side

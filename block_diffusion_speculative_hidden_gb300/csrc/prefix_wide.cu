@@ -562,10 +562,10 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     __syncwarp();
     tc_fence_after();
     l += partner(n & 1, l);
-    float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+    float lse2 = l != 0.f ? m + log2f(l) : -INFINITY;  // (l is a NaN where a score is one)
     float x[DH / 2];  // the row's result, this half's dimensions
     {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
       for (int d = 0; d < DH / 2; d += 16) {
         uint32_t v[16];
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
           tc_wait_ld();
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[d + e] = l > 0.f ? __uint_as_float(v[e]) * inv : 0.f;
+        for (int e = 0; e < 16; ++e) x[d + e] = l != 0.f ? __uint_as_float(v[e]) * inv : 0.f;
       }
     }
     const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
@@ -599,21 +599,21 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
 #pragma unroll
         for (int d = 0; d < DH / 2; d += 4) {
           const float4 y = *reinterpret_cast<const float4*>(stage + (DH / 2 * half + d) * 4);
-          x[d] = x[d] * f0 + (f1 > 0.f ? y.x * f1 : 0.f);
-          x[d + 1] = x[d + 1] * f0 + (f1 > 0.f ? y.y * f1 : 0.f);
-          x[d + 2] = x[d + 2] * f0 + (f1 > 0.f ? y.z * f1 : 0.f);
-          x[d + 3] = x[d + 3] * f0 + (f1 > 0.f ? y.w * f1 : 0.f);
+          x[d] = x[d] * f0 + (f1 != 0.f ? y.x * f1 : 0.f);
+          x[d + 1] = x[d + 1] * f0 + (f1 != 0.f ? y.y * f1 : 0.f);
+          x[d + 2] = x[d + 2] * f0 + (f1 != 0.f ? y.z * f1 : 0.f);
+          x[d + 3] = x[d + 3] * f0 + (f1 != 0.f ? y.w * f1 : 0.f);
         }
         // (x and weight are relative to 2^top; the first term's weight is 1 where it has any)
-        weight = (lse2 > -INFINITY ? weight * f0 : 0.f) + f1;
+        weight = (lse2 != -INFINITY ? weight * f0 : 0.f) + f1;
         lse2 = top;
         fence_proxy_async_smem();
         wide_bar(pair, 64);  // both halves are through with the copy
       }
-      const float inv = weight > 0.f ? 1.f / weight : 0.f;
+      const float inv = weight != 0.f ? 1.f / weight : 0.f;
 #pragma unroll
       for (int d = 0; d < DH / 2; ++d) x[d] *= inv;
-      lse2 = weight > 0.f ? lse2 + log2f(weight) : -INFINITY;
+      lse2 = weight != 0.f ? lse2 + log2f(weight) : -INFINITY;
     }
     if (it.last) {
 #pragma unroll

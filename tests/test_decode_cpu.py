@@ -69,6 +69,7 @@ def test_attention_refusals(L):
     assert _attend(L, _kv(head_dim=32)) == UNSUPPORTED
     assert _attend(L, _kv(head_dim=96), ld_q=400) == UNSUPPORTED
     assert _attend(L, T=1 << 29) == UNSUPPORTED
+    assert _attend(L, B=4097, seq=P) == UNSUPPORTED and _attend(L, NG=4097) == UNSUPPORTED
     assert _attend(L, ws_bytes=255) == WORKSPACE
 
 

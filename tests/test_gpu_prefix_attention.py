@@ -295,3 +295,56 @@ def test_drafter_cache_with_a_shared_prefix():
         check_attention(C, q, out, lse, [3, 3], [0, 1], [(0, 2, 2)], True, 1 / math.sqrt(cfg.head_dim))
     assert dr.device_status() == 0
     dr.close()
+
+
+def test_many_short_sequences():
+    """More entries than the CTAs keep in shared memory, several of them a warp; most and fewest that a call takes."""
+    lens = [(7 * b) % 41 for b in range(600)]
+    _run(600, 1, 4, 1, 64, "float16", lens)
+    _run(600, 2, 4, 1, 128, "bfloat16", lens, [(2, (13 * g) % 70) for g in range(300)], n=[b % 3 for b in range(600)])
+    _run(4096, 1, 2, 1, 64, "float16", [b % 5 for b in range(4096)], [(2, g % 3 * 9) for g in range(2048)])
+
+
+def test_short_prefixes_of_few_rows():
+    # groups of 8 rows and fewer a kv head: prefixes and own parts on one line of pages
+    _run(7, 1, 8, 4, 64, "bfloat16", [5, 0, 17, 300, 33, 1, 64], [(1, 40), (3, 500), (0, 16), (1, None), (2, 129)])
+    _run(4, 2, 8, 2, 128, "float16", [2, 18, 90, 5], [(1, 1000), (1, 17), (1, 0), (1, 64)], n=[1, 0, 2, 2])
+    # on average: one group has 40 rows
+    _run(25, 1, 4, 1, 64, "float16", [3 * b for b in range(25)], [(1, 33)] * 15 + [(10, 250)])
+
+
+@pytest.mark.parametrize("dtype,dh,Hq,Hkv,B", [("float16", 64, 64, 8, 44), ("bfloat16", 128, 24, 8, 112)])
+def test_live_rows_of_a_large_batch(dtype, dh, Hq, Hkv, B):
+    """Row tiles that hold live rows of several entries, some of them without any."""
+    n = [(5 * b + 3) % 17 for b in range(B)]
+    lens = [(37 * b) % 90 for b in range(B)]
+    for rows in (n, [16] * B, [0] * 9 + [1] * (B - 9)):
+        _run(B, 16, Hq, Hkv, dh, dtype, lens, [(9, 260), (0, 70), (3, None), (B - 13, 700), (1, 31)], n=rows)
+    _run(B, 16, Hq, Hkv, dh, dtype, lens, [(B, 150)], n=n, causal=False, in_place=False)
+
+
+@pytest.mark.parametrize("T", [1, 17])
+def test_nan_stays_in_its_rows(T):
+    """A NaN query gives NaN in its row and in no other; a NaN key that no row sees gives none."""
+    import torch
+    from block_diffusion_speculative_hidden_gb300 import prefix_attention
+    from decode_ref import Cache, check_attention
+    for dh in (64, 128):
+        c = Cache([T + 40, T, 500], 2, dh, torch.float16, 9)
+        q = torch.randn(2, T, 8, dh, device="cuda", dtype=torch.float16)
+        want, lw = torch.empty_like(q), torch.empty(2, T, 8, device="cuda")
+        prefix_attention(c.paged(), q, _ints([0, 2]), _ints([2]), out=want, lse=lw)
+        check_attention(c, q, want, lw, [T, T], [0, 1], [(0, 2, 2)], True, 1 / math.sqrt(dh))
+        bad = q.clone()
+        bad[1, T - 1, 3, 5] = math.nan
+        out, lse = torch.empty_like(q), torch.empty(2, T, 8, device="cuda")
+        prefix_attention(c.paged(), bad, _ints([0, 2]), _ints([2]), out=out, lse=lse)
+        assert out[1, T - 1, 3].isnan().all() and lse[1, T - 1, 3].isnan()
+        out[1, T - 1, 3], lse[1, T - 1, 3] = want[1, T - 1, 3], lw[1, T - 1, 3]
+        check_attention(c, q, out, lse, [T, T], [0, 1], [(0, 2, 2)], True, 1 / math.sqrt(dh))
+        if T > 1:                                # the last token's key: rows before it do not see it
+            page, slot = c.table[0].long()[(T + 39) // 16], (T + 39) % 16
+            c.k[page, :, slot] = math.nan
+            prefix_attention(c.paged(), q, _ints([0, 2]), _ints([2]), out=out, lse=lse)
+            assert out[0, T - 1].isnan().all() and torch.isfinite(out[0, :T - 1].float()).all()
+            assert torch.isfinite(out[1].float()).all()

@@ -66,6 +66,30 @@ def test_wide():
     _check(20, 24576, 1024, 128, zero=True)
 
 
+@pytest.mark.parametrize("M", [1, 8, 16])
+def test_many_tiles_and_parts_of_k(M):
+    """Several tiles a warp; activations of which shared memory holds a part at a time."""
+    _check(M, 24576, 512, 64, zero=True, x="float16", scale="float16")
+    _check(M, 40000, 768, 32, "e2m1")
+    _check(M, 2500, 12416, 128, zero=True)
+    _check(M, 300, 33024, 32, "e2m1", scale="float32")
+    _check(M, 48, 16640, 32, zero=True, scale="float32")
+
+
+def test_scales_and_zero_points_at_any_address():
+    import torch
+    from block_diffusion_speculative_hidden_gb300 import gemm_w4
+    from decode_ref import check_w4
+    for group, M in ((32, 1), (64, 9), (128, 16), (128, 17)):
+        W, sc, X, z = _data(M, 70, 1024, group, "int4", True, "bfloat16", "float16")
+        for shift in (1, 2, 3, 4, 8):
+            s2 = torch.zeros(sc.numel() + 8, dtype=sc.dtype, device="cuda")[shift:shift + sc.numel()].view_as(sc)
+            z2 = torch.zeros(z.numel() + 8, dtype=z.dtype, device="cuda")[shift:shift + z.numel()].view_as(z)
+            s2.copy_(sc)
+            z2.copy_(z)
+            check_w4(gemm_w4(W, s2, X, zero=z2, group=group), W, sc, X, z, group, "int4")
+
+
 def test_offsets_past_32_bits():
     """N * K / 2 > 2^31 bytes of codes: the last rows."""
     import torch
