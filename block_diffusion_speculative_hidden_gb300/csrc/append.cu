@@ -78,6 +78,11 @@ struct AppendParams {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendHeads = 2;  // (1: 9.2 us for verified blocks, 2: 8.3, 4: 9.6, for their registers)
 
+// Bound by memory: every byte is read and written once (128 blocks of up to 17
+// rows, 64 query and 8 kv heads of 64 from fp32 to fp16: 8.1 us, 4.4 TB/s, of
+// which 2.5 us are a launch; 8 prompts of up to 4096 rows, 8 kv heads of 128:
+// 33.5 us, 5.5 TB/s).
+//
 // DH / 16 threads take kAppendHeads heads of one row, each eight elements of
 // the heads' first halves and the eight that they rotate with: the angles are
 // read once for those heads, and their elements are on the way while the

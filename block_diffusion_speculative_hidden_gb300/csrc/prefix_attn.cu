@@ -7,9 +7,12 @@
 // exp(z - l_S) v, and
 //     out = sum_S exp(l_S - l) o_S,  l = log sum_S exp l_S.
 // So a prefix is read once for all query rows of its group (as one tall
-// matrix of rows), each sequence's own keys for its own rows, either of them
-// in several chunks of pages, and a last kernel joins the partial results in
-// a fixed order.
+// matrix of rows) and each sequence's own keys for its own rows.  Parts of
+// more than 8 rows are the wide kernel's (prefix_wide.cu: tcgen05, chunks of
+// pages), those of fewer the thin one's (here: mma.sync, warps that stream
+// pages).  Partial results are joined in a fixed order: by the wide kernel's
+// own parts where they are whole and the prefix has at most four chunks, else
+// by a kernel of its own.
 #include <algorithm>
 
 #include "prefix_common.cuh"
@@ -175,6 +178,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // takes, and its own running maxima, sums and outputs.  The products are taken
 // transposed, S^T = K Q^T and O^T = V^T P^T, so that keys and dimensions fill
 // the 16 rows of an MMA and the query rows its 8 columns.
+//
+// Bound by memory while it streams (64 sequences, 8 kv heads of 128: from 1024
+// to 1500 tokens 125 MB in 18.4 us, 6.8 TB/s); what is left is what a call takes
+// to start and to join: 64 sequences of 1024 tokens take 51 us, 5.2 TB/s, one
+// of 77 tokens 7.1.  Until a warp's first page is there: 1.3 us for the line,
+// 1.4 for the first page ids, 1.2 for the copy.
 template <typename T16, int DH>
 __global__ void __launch_bounds__(ThinLayout<DH>::THREADS) k_prefix_thin(const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV,
@@ -392,31 +401,29 @@ __global__ void __launch_bounds__(ThinLayout<DH>::THREADS) k_prefix_thin(const _
 constexpr int kJoinWarps = 8;
 
 // out of the partial results: `share` warps (1 or 8) a query row, each adding
-// every share-th part.  Parts: of the prefix, then of the entry's own sequence;
+// every share-th part, and `rows` rows one after the other (an entry's rows have
+// its lookups in common).  Parts: of the prefix, then of the entry's own sequence;
 // the wide kernel leaves them by chunk, the thin one as said above.
 template <typename T16, int DH>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, int share) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, int share, int rows) {
   using M = Mma16<T16>;
   constexpr int E = DH / 32;  // elements a lane
   __shared__ float s_a[kJoinWarps][DH], s_sum[kJoinWarps], s_top[kJoinWarps];
   __shared__ long long s_first[kThinHeld + 1], s_scan[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % share;
-  const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-  const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / share) + warp / share;
-  const long long tok = row / p.Hq;
-  const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
-  const int h = static_cast<int>(row - tok * p.Hq), kvh = h / p.G;
-  const bool live = row < R && t < entry_rows(p, b);
-  // [0] the prefix's parts, [1] the own ones: how many, and where they are
-  int n[2] = {0, 0}, lane_row[2] = {0, 0};
-  long long f0[2] = {0, 0}, w0[2] = {0, 0};  // (thin) first page on the line, and the warp that takes it
-  long long per = 1;
+  const int R = p.B * p.T * p.Hq;  // (below 2^30)
+  const int row0 = (blockIdx.x * (kJoinWarps / share) + warp / share) * rows;
+  int at_b = -1, rows_b = 0, own = 0;
   Group g{0, 0, -1, 0, 0, 0};
-  int own = 0;
-  if (live) {
+  auto entry = [&](int row) {  // what the row's entry has, once for all its rows
+    const int b = row / (p.Hq * p.T);
+    if (row >= R || b == at_b) return;
+    at_b = b;
+    rows_b = entry_rows(p, b);
     g = group_of(p, b);
     own = pages_of(seq_tokens(p, p.seq != nullptr ? p.seq[b] : b));
-  }
+  };
+  entry(row0);
   // the thin kernel's line (a long one is read where that kernel left it)
   const int groups = p.p_thin ? p.NG : 0;
   const bool held = groups + p.B <= kThinHeld;
@@ -424,111 +431,121 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
   if (p.warps > 0 && held)
     thin_line<kJoinWarps>(p, groups, p.NG == 0 || bounds_ok(p), false, s_first, nullptr, s_scan);
   if (!held) pdl_wait();
-  if (live) {
-    const int pre = pages_of(g.tokens);
-    if (p.p_chunks > 0) n[0] = chunks_of(pre, p.p_chunks);
-    if (p.s_chunks > 0) n[1] = chunks_of(own, p.s_chunks);
-    if (p.warps > 0) per = thin_per(first[groups + p.B], p.warps);
-    auto on_line = [&](int which, int e, int pages, int r) {
-      f0[which] = first[e] + static_cast<long long>(r / kThinRows * p.Hkv + kvh) * pages;
-      w0[which] = thin_div(f0[which], per);
-      lane_row[which] = r % kThinRows;
-      n[which] = pages > 0 ? static_cast<int>(thin_div(f0[which] + pages - 1, per) - w0[which]) + 1 : 0;
-    };
-    const int gi = h - kvh * p.G;
-    if (p.p_thin && pre > 0) on_line(0, g.index, pre, ((b - g.lo) * p.T + t) * p.G + gi);
-    if (p.s_chunks == 0) on_line(1, groups + b, own, t * p.G + gi);
-  }
-  const int n_all = n[0] + n[1];
-  // where part c is: its log-sum-exp, and its output
-  auto place = [&](int c, const float*& lse, const float*& o) {
-    const int which = c < n[0] ? 0 : 1, k = which ? c - n[0] : c;
-    long long at;
-    if (which ? p.s_chunks > 0 : p.p_chunks > 0) {
-      at = static_cast<long long>(which ? p.p_chunks + k : k) * R + row;
-      lse = p.part_lse;
-      o = p.part_o;
-    } else if (n[which] == 1) {
-      at = which * R + row;
-      lse = p.whole_lse;
-      o = p.whole_o;
-    } else {
-      const long long w = w0[which] + k;
-      at = (2 * w + (k > 0 || f0[which] == w * per ? 0 : 1)) * kThinRows + lane_row[which];
-      lse = p.slot_lse;
-      o = p.slot_o;
+  for (int i = 0; i < rows; ++i) {
+    const int row = row0 + i;
+    entry(row);
+    const int tok = row / p.Hq, b = tok / p.T, t = tok - b * p.T, h = row - tok * p.Hq, kvh = h / p.G;
+    const bool live = row < R && t < rows_b;
+    // [0] the prefix's parts, [1] the own ones: how many, and where they are
+    int n[2] = {0, 0}, lane_row[2] = {0, 0};
+    long long f0[2] = {0, 0}, w0[2] = {0, 0};  // (thin) first page on the line, and the warp that takes it
+    long long per = 1;
+    if (live) {
+      const int pre = pages_of(g.tokens);
+      if (p.p_chunks > 0) n[0] = chunks_of(pre, p.p_chunks);
+      if (p.s_chunks > 0) n[1] = chunks_of(own, p.s_chunks);
+      if (p.warps > 0) per = thin_per(first[groups + p.B], p.warps);
+      auto on_line = [&](int which, int e, int pages, int r) {
+        f0[which] = first[e] + static_cast<long long>(r / kThinRows * p.Hkv + kvh) * pages;
+        w0[which] = thin_div(f0[which], per);
+        lane_row[which] = r % kThinRows;
+        n[which] = pages > 0 ? static_cast<int>(thin_div(f0[which] + pages - 1, per) - w0[which]) + 1 : 0;
+      };
+      const int gi = h - kvh * p.G;
+      if (p.p_thin && pre > 0) on_line(0, g.index, pre, ((b - g.lo) * p.T + t) * p.G + gi);
+      if (p.s_chunks == 0) on_line(1, groups + b, own, t * p.G + gi);
     }
-    lse += at;
-    o += at * DH;
-  };
-  // kJoinParts parts at a time: a lane finds one and its weight, then all add
-  // them up.  What they need from before is found first, so that one wait for
-  // memory is left once the partial results are there.
-  constexpr int kJoinParts = 16;
-  float mx = -INFINITY, sum = 0.f, a[E] = {};
-  for (int c0 = 0; c0 * share + sub < n_all || c0 == 0; c0 += kJoinParts) {
-    const int c = (c0 + (lane & (kJoinParts - 1))) * share + sub;
-    const int count = min(kJoinParts, (n_all - sub + share - 1) / share - c0);
-    const float *lse = nullptr, *mine = nullptr;
-    if (c < n_all) place(c, lse, mine);
-    const unsigned long long addr = reinterpret_cast<unsigned long long>(mine);
-    if (c0 == 0 && held) pdl_wait();
-    const float z = c < n_all && lane < kJoinParts ? *lse : -INFINITY;
-    float v[kJoinParts][E];
-#pragma unroll
-    for (int k = 0; k < kJoinParts; ++k) {
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, k)) + lane * E;
-      if (k >= count) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
-      } else if constexpr (E == 4) {
-        *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+    const int n_all = n[0] + n[1];
+    // where part c is: its log-sum-exp, and its output
+    auto place = [&](int c, const float*& lse, const float*& o) {
+      const int which = c < n[0] ? 0 : 1, k = which ? c - n[0] : c;
+      long long at;
+      if (which ? p.s_chunks > 0 : p.p_chunks > 0) {
+        at = (which ? p.p_chunks + k : k) * static_cast<long long>(R) + row;
+        lse = p.part_lse;
+        o = p.part_o;
+      } else if (n[which] == 1) {
+        at = which * static_cast<long long>(R) + row;
+        lse = p.whole_lse;
+        o = p.whole_o;
       } else {
-        *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+        const long long w = w0[which] + k;
+        at = (2 * w + (k > 0 || f0[which] == w * per ? 0 : 1)) * kThinRows + lane_row[which];
+        lse = p.slot_lse;
+        o = p.slot_o;
+      }
+      lse += at;
+      o += at * DH;
+    };
+    // kJoinParts parts at a time: a lane finds one and its weight, then all add
+    // them up.  What they need from before is found first, so that one wait for
+    // memory is left once the partial results are there.
+    constexpr int kJoinParts = 16;
+    float mx = -INFINITY, sum = 0.f, a[E] = {};
+    for (int c0 = 0; c0 * share + sub < n_all || c0 == 0; c0 += kJoinParts) {
+      const int c = (c0 + (lane & (kJoinParts - 1))) * share + sub;
+      const int count = min(kJoinParts, (n_all - sub + share - 1) / share - c0);
+      const float *lse = nullptr, *mine = nullptr;
+      if (c < n_all) place(c, lse, mine);
+      const unsigned long long addr = reinterpret_cast<unsigned long long>(mine);
+      if (c0 == 0 && i == 0 && held) pdl_wait();
+      const float z = c < n_all && lane < kJoinParts ? *lse : -INFINITY;
+      float v[kJoinParts][E];
+#pragma unroll
+      for (int k = 0; k < kJoinParts; ++k) {
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, k)) + lane * E;
+        if (k >= count) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+        } else if constexpr (E == 4) {
+          *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+        } else {
+          *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+        }
+      }
+      const float top = fmaxf(mx, warp_max(z)), at = top == -INFINITY ? 0.f : top;
+      const float keep = exp2f(mx - at), f = exp2f(z - at);
+      mx = top;
+      sum = sum * keep + warp_sum(f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] *= keep;
+#pragma unroll
+      for (int k = 0; k < kJoinParts; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] += w * v[k][e];
       }
     }
-    const float top = fmaxf(mx, warp_max(z)), at = top == -INFINITY ? 0.f : top;
-    const float keep = exp2f(mx - at), f = exp2f(z - at);
-    mx = top;
-    sum = sum * keep + warp_sum(f);
+    if (share > 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) a[e] *= keep;
+      for (int e = 0; e < E; ++e) s_a[warp][lane * E + e] = a[e];
+      if (lane == 0) {
+        s_sum[warp] = sum;
+        s_top[warp] = mx;
+      }
+      __syncthreads();
+      if (warp != 0) return;
+      for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, s_top[w]);
+      const float at = mx == -INFINITY ? 0.f : mx;
+      sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < kJoinParts; ++k) {
-      const float w = __shfl_sync(0xffffffffu, f, k);
+      for (int e = 0; e < E; ++e) a[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] += w * v[k][e];
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = exp2f(s_top[w] - at);
+        sum += f * s_sum[w];
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] += f * s_a[w][lane * E + e];
+      }
     }
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    if (!live) continue;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    T16* dst = static_cast<T16*>(p.out) + static_cast<long long>(row) * DH + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = M::pack(a[e] * inv, a[e + 1] * inv);
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = sum != 0.f ? (ms + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
-  if (share > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_a[warp][lane * E + e] = a[e];
-    if (lane == 0) {
-      s_sum[warp] = sum;
-      s_top[warp] = mx;
-    }
-    __syncthreads();
-    if (warp != 0) return;
-    for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, s_top[w]);
-    const float at = mx == -INFINITY ? 0.f : mx;
-    sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) a[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = exp2f(s_top[w] - at);
-      sum += f * s_sum[w];
-#pragma unroll
-      for (int e = 0; e < E; ++e) a[e] += f * s_a[w][lane * E + e];
-    }
-  }
-  const float ms = mx == -INFINITY ? 0.f : mx;
-  if (!live) return;
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  T16* dst = static_cast<T16*>(p.out) + row * DH + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = M::pack(a[e] * inv, a[e + 1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum != 0.f ? (ms + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host side
@@ -547,6 +564,7 @@ struct PrefixPlan {
   bool merge, join;            // own parts add the prefix's partial results; a kernel joins them all
   long long p_tiles, s_tiles;  // row tiles of the wide kernel: of all groups (a bound), of an entry
   long long rows;
+  int sms;
   int p_chunks, s_chunks;      // of the wide kernel's parts (0: the thin kernel's)
   int warps;                   // of the thin kernel (0: not used)
   size_t off_work, off_lse, off_o, off_whole_lse, off_whole_o, off_slot_lse, off_slot_o, bytes;
@@ -595,6 +613,7 @@ bool make_plan(const dflash_paged_kv& kv, int Hq, int B, int T, int NG, int max_
   r.s_wide = fits && tg >= kWideFrom;
   r.p_wide = fits && NG > 0 && (r.s_wide || B * tg >= static_cast<long long>(kWideFrom) * NG);
   const int sms = plan_sms(), rows = wide_rows(std::min(G, kWideTile));
+  r.sms = sms;
   if (r.p_wide) {
     r.p_tiles = (B * tg + static_cast<long long>(NG) * (rows - 1)) / rows;
     // Packing the live rows takes a tile longer (3 us, and 4 percent of the loop)
@@ -719,9 +738,12 @@ cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int ele
                     : launch_thin<T16, DH>(p, plan.p_wide, m.thin_k, m.thin_v, s);
   if (e != cudaSuccess || !plan.join) return e;
   // few rows: a row's parts over all the warps of a CTA
-  const int share = plan.rows < 8ll * 152 ? kJoinWarps : 1, per = kJoinWarps / share;
+  // (many rows: as many warps as the SMs hold at once take several)
+  const int share = plan.rows < 8ll * plan.sms ? kJoinWarps : 1;
+  const int rows = static_cast<int>((plan.rows + 32ll * plan.sms - 1) / (32ll * plan.sms));
+  const long long per = static_cast<long long>(kJoinWarps / share) * rows;
   return launch_k(k_prefix_join<T16, DH>, dim3(static_cast<unsigned>((plan.rows + per - 1) / per)),
-                  dim3(kJoinWarps * 32), 0, s, dim3(1), true, p, share);
+                  dim3(kJoinWarps * 32), 0, s, dim3(1), true, p, share, rows);
 }
 
 }  // namespace

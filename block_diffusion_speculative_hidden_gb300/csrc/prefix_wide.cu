@@ -10,6 +10,14 @@
 // maximum of a row's first tile and moves (O is then rescaled in TMEM) only
 // when a later tile's P sums to 2^14 or more, so P stays within 16 bits and
 // most tiles need no maximum.
+//
+// Of 128 query rows and 128 keys with 128 dimensions an SM makes one product
+// pair in 0.95 us (two CTAs, 1060 TFLOP/s over the card; 0.66 us would be the
+// matrix units'): the latencies between the softmax's steps keep them from more
+// (issue slots 0.49 taken, matrix units 0.46, exponentials 0.23).  32 entries
+// of 17 rows, 32 query heads on 8 kv heads: a prefix of 8192 75 us, 16384 135;
+// own sequences of 700 22 us.  With two S of 64 keys in the place of one of 128
+// (S of the next half under the softmax) the same prefixes take 76 and 136 us.
 #include "prefix_common.cuh"
 
 namespace dflash {

@@ -69,7 +69,7 @@ class PagedKV:
     [n_pages, n_kv_heads, 16, head_dim] (fp32, bf16 or fp16), page_table int32
     [n_seqs, max_pages], seq_len int32 [n_seqs]."""
 
-    __slots__ = ("k", "v", "page_table", "seq_len", "dev", "view", "ref")
+    __slots__ = ("k", "v", "page_table", "seq_len", "dev", "shape", "view", "ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
         n, h, page, dh = k.shape
@@ -85,8 +85,9 @@ class PagedKV:
         _need(v.get_device() == dev and page_table.get_device() == dev and seq_len.get_device() == dev,
               "one device for the whole cache")
         self.k, self.v, self.page_table, self.seq_len, self.dev = k, v, page_table, seq_len, dev
-        self.view = _lib.DflashPagedKV(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_len.data_ptr(), n, rows,
-                                       most, h, dh, _ELEM[dt])
+        self.shape = (n, rows, most, h, dh, _ELEM[dt])
+        self.view = _lib.DflashPagedKV(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_len.data_ptr(),
+                                       *self.shape)
         self.ref = ctypes.byref(self.view)
 
 
@@ -119,9 +120,9 @@ def append_kv(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, n_rows: Optional[to
         with guard:
             return append_kv(kv, k, v, n_rows, seq=seq, pos_base=pos_base, rope=rope, q=q, q_out=q_out, status=status)
     B, T, H, dh = k.shape
-    w, src = kv.view, k.dtype
+    src = k.dtype
     _need(v.shape == k.shape and v.dtype is src and src in _ELEM, "k, v: [B, T, n_kv_heads, head_dim] of one type")
-    _need(H == w.n_kv_heads and dh == w.head_dim, "k, v do not have the cache's heads")
+    _need((H, dh) == kv.shape[3:5], "k, v do not have the cache's heads")
     _need(k.get_device() == dev and v.get_device() == dev, "k, v are on another device than the cache")
     cos = sin = qp = op = None
     rows = ld_q = Hq = 0
@@ -151,8 +152,8 @@ def append_kv(kv: PagedKV, k: torch.Tensor, v: torch.Tensor, n_rows: Optional[to
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(n_pages, n_seqs, max_pages, Hkv, dh, elem, Hq, B, T, NG, max_prefix, max_len, dev):
-    view = _lib.DflashPagedKV(256, 256, 256, 256, n_pages, n_seqs, max_pages, Hkv, dh, elem)
+def _workspace_bytes(shape, Hq, B, T, NG, max_prefix, max_len, dev):
+    view = _lib.DflashPagedKV(256, 256, 256, 256, *shape)
     return _lib.lib().dflash_prefix_attention_workspace(ctypes.byref(view), Hq, B, T, NG, max_prefix, max_len)
 
 
@@ -163,9 +164,7 @@ def prefix_attention_workspace(kv: PagedKV, n_q_heads: int, B: int, T: int, n_gr
     if guard is not None:
         with guard:
             return prefix_attention_workspace(kv, n_q_heads, B, T, n_groups, max_prefix, max_len)
-    w = kv.view
-    return _workspace_bytes(w.n_pages, w.n_seqs, w.max_pages, w.n_kv_heads, w.head_dim, w.elem, n_q_heads, B, T,
-                            n_groups, max_prefix, max_len, kv.dev)
+    return _workspace_bytes(kv.shape, n_q_heads, B, T, n_groups, max_prefix, max_len, kv.dev)
 
 
 def prefix_attention(kv: PagedKV, q: torch.Tensor, group_off: Optional[torch.Tensor] = None,
@@ -189,8 +188,8 @@ def prefix_attention(kv: PagedKV, q: torch.Tensor, group_off: Optional[torch.Ten
                                     max_prefix=max_prefix, max_len=max_len, out=out, lse=lse, workspace=workspace,
                                     status=status)
     B, T, Hq, dh = q.shape
-    w, dt = kv.view, q.dtype
-    _need(dt is kv.k.dtype and dh == w.head_dim and q.get_device() == dev,
+    dt = q.dtype
+    _need(dt is kv.k.dtype and dh == kv.shape[4] and q.get_device() == dev,
           "q: [B, T, n_q_heads, head_dim] of the cache's type, head_dim and device")
     NG = off = pre = 0
     if group_off is not None or prefix_seq is not None:
@@ -207,8 +206,7 @@ def prefix_attention(kv: PagedKV, q: torch.Tensor, group_off: Optional[torch.Ten
               "lse: contiguous fp32 [B, T, n_q_heads]")
         lp = lse.data_ptr()
     if workspace is None:
-        size = _workspace_bytes(w.n_pages, w.n_seqs, w.max_pages, w.n_kv_heads, w.head_dim, w.elem, Hq, B, T, NG,
-                                max_prefix, max_len, dev)
+        size = _workspace_bytes(kv.shape, Hq, B, T, NG, max_prefix, max_len, dev)
         workspace = torch.empty(size or 256, dtype=_U8, device=q.device)
     else:
         _need(workspace.get_device() == dev and workspace.is_contiguous(), "workspace: contiguous, the cache's device")
