@@ -52,7 +52,7 @@ struct WideLayout {
   static constexpr uint32_t P_PAGE = P_APART ? 8 : 16, COLS = 256;
   static_assert(O_COL + DH <= COLS, "the accumulators fit TMEM");
   static_assert(SMEM <= 115712, "shared memory of a CTA");
-  static_assert((2 * NS + 6) * 8 + 8 <= 256, "barriers fit their area");
+  static_assert((2 * NS + 5) * 8 + 8 <= 256, "barriers fit their area");
   // the CTAs that an SM can hold by their shared memory find room in its 512
   // TMEM columns: an allocation never waits for another CTA's
   static_assert((512 / COLS + 1) * (SMEM + 1024) > 233472, "no more CTAs an SM than TMEM has room for");
@@ -100,11 +100,20 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(token), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void bulk_store_row(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
+// Rows between shared memory (32 rows of a pair of warps from `stage` on, pitch
+// apart) and global memory: the whole warp takes row after row of its 16, so
+// that a row or two cost one instruction (bulk copies of a row a thread are
+// issued one thread at a time: 1.4 us for 32).  at: the row of lane l, -1: none.
+template <int BYTES, typename Each>
+__device__ __forceinline__ void wide_rows_each(uint8_t* stage, int pitch, int half, int at, Each&& each) {
+  constexpr int LANES = BYTES / 16, ROWS = 32 / LANES;  // of a row; at once
+  const int lane = threadIdx.x & 31, piece = lane % LANES;
+#pragma unroll
+  for (int i = 0; i < 16; i += ROWS) {
+    const int r = half * 16 + i + lane / LANES, a = __shfl_sync(0xffffffffu, at, r);
+    if (a >= 0) each(stage + r * pitch + piece * 16, static_cast<long long>(a) * BYTES + piece * 16);
+  }
 }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Instruction descriptor of tcgen05.mma kind::f16 with fp32 accumulators: A
 // and B fp16 or bf16, B transposed (its N dimension contiguous) for P V.
@@ -231,8 +240,7 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
   uint64_t* s_read = s_full + 1;  // S is in registers (P_APART)
   uint64_t* p_full = s_read + 1;
   uint64_t* o_full = p_full + 1;
-  uint64_t* part_full = o_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_full + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
   // (through a shuffle, so that what follows from it is known to be alike in a warp)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   constexpr int kTmaWarp = L::SOFT, kMmaWarp = L::SOFT + 1;
@@ -276,7 +284,6 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
     mbar_init(s_read, 256);
     mbar_init(p_full, 256);
     mbar_init(o_full, 1);
-    mbar_init(part_full, kWideTile);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -586,24 +593,21 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
       }
     }
     const long long R = static_cast<long long>(p.B) * p.T * p.Hq;
-    uint8_t* stage = smem + r * L::PITCH;
+    uint8_t *rows = smem + quad * 32 * L::PITCH, *stage = rows + lane * L::PITCH;  // the pair's, this one
     if (it.last && parts > 0) {
       // add the prefix's partial results, a copy of the row at a time (in order)
       pdl_wait();
       float weight = 1.f;
       for (int c = 0; c < parts; ++c) {
-        if (half == 0) {
-          if (at >= 0) {
-            mbar_arrive_expect_tx(part_full, DH * 4);
-            bulk_load_global(smem_u32(stage), p.part_o + (c * R + at) * DH, DH * 4, part_full);
-          } else {
-            mbarrier_arrive_one(part_full);
-          }
-        }
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(p.part_o + c * R * DH);
+        wide_rows_each<DH * 4>(rows, L::PITCH, half, at, [&](uint8_t* d, long long o) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d)), "l"(from + o) : "memory");
+        });
         const float other = at >= 0 ? p.part_lse[c * R + at] : -INFINITY;
         const float top = fmaxf(lse2, other), base = top == -INFINITY ? 0.f : top;
         const float f0 = wide_ex2(lse2 - base), f1 = wide_ex2(other - base);
-        ok = ok && mbar_wait(part_full, c & 1, p.status);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        wide_bar(pair, 64);
 #pragma unroll
         for (int d = 0; d < DH / 2; d += 4) {
           const float4 y = *reinterpret_cast<const float4*>(stage + (DH / 2 * half + d) * 4);
@@ -615,7 +619,6 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
         // (x and weight are relative to 2^top; the first term's weight is 1 where it has any)
         weight = (lse2 != -INFINITY ? weight * f0 : 0.f) + f1;
         lse2 = top;
-        fence_proxy_async_smem();
         wide_bar(pair, 64);  // both halves are through with the copy
       }
       const float inv = weight != 0.f ? 1.f / weight : 0.f;
@@ -634,19 +637,19 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
       for (int d = 0; d < DH / 2; d += 4)
         *reinterpret_cast<float4*>(stage + (DH / 2 * half + d) * 4) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
     }
-    fence_proxy_async_smem();
     wide_bar(pair, 64);
-    if (at >= 0 && half == 0) {
-      const long long part = (it.shared ? it.chunk : p.p_chunks + it.chunk) * R + at;
-      if (it.last) {
-        bulk_store_row(static_cast<T16*>(p.out) + at * DH, smem_u32(stage), DH * 2);
-        if (p.lse != nullptr) p.lse[at] = lse2 * 0.69314718055994531f;
-      } else {
-        bulk_store_row(p.part_o + part * DH, smem_u32(stage), DH * 4);
-        p.part_lse[part] = lse2;
-      }
-      bulk_commit();
-      bulk_wait_all();
+    const long long part = (it.shared ? it.chunk : p.p_chunks + it.chunk) * R;
+    if (it.last) {
+      wide_rows_each<DH * 2>(rows, L::PITCH, half, at, [&](uint8_t* d, long long o) {
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + o) = *reinterpret_cast<const uint4*>(d);
+      });
+      if (at >= 0 && half == 0 && p.lse != nullptr) p.lse[at] = lse2 * 0.69314718055994531f;
+    } else {
+      uint8_t* to = reinterpret_cast<uint8_t*>(p.part_o + part * DH);
+      wide_rows_each<DH * 4>(rows, L::PITCH, half, at, [&](uint8_t* d, long long o) {
+        *reinterpret_cast<uint4*>(to + o) = *reinterpret_cast<const uint4*>(d);
+      });
+      if (at >= 0 && half == 0) p.part_lse[part + at] = lse2;
     }
   }
   tc_fence_before();

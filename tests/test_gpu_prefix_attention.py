@@ -348,3 +348,21 @@ def test_nan_stays_in_its_rows(T):
             prefix_attention(c.paged(), q, _ints([0, 2]), _ints([2]), out=out, lse=lse)
             assert out[0, T - 1].isnan().all() and torch.isfinite(out[0, :T - 1].float()).all()
             assert torch.isfinite(out[1].float()).all()
+
+
+@pytest.mark.parametrize("P", [0, 200])
+def test_more_than_32_bits_of_rows(P):
+    """B T Hq head_dim past 2^31: the last entries of a batch whose other ones have no rows."""
+    import torch
+    from block_diffusion_speculative_hidden_gb300 import prefix_attention
+    from decode_ref import Cache, check_attention
+    B, T, Hq, dh = 4096, 65, 64, 128
+    assert B * T * Hq * dh > 1 << 31
+    c = Cache([70, 90, 0, 200], 8, dh, torch.bfloat16, 3)
+    q = torch.zeros(B, T, Hq, dh, device="cuda", dtype=torch.bfloat16)
+    q[-2:] = torch.randn(2, T, Hq, dh, device="cuda").bfloat16()
+    out, lse = torch.empty_like(q), torch.empty(B, T, Hq, device="cuda")
+    n, seq = [0] * (B - 2) + [T, 3], [2] * (B - 2) + [0, 1]
+    groups = dict(group_off=_ints([0, B]), prefix_seq=_ints([3]), max_prefix=P) if P else {}
+    prefix_attention(c.paged(), q, n_rows=_ints(n), seq=_ints(seq), max_len=90, out=out, lse=lse, **groups)
+    check_attention(c, q, out, lse, n, seq, [(0, B, 3)] if P else [], True, 1 / math.sqrt(dh))
