@@ -404,7 +404,7 @@ constexpr int kJoinWarps = 8;
 // every share-th part, and `rows` rows one after the other (an entry's rows have
 // its lookups in common).  Parts: of the prefix, then of the entry's own sequence;
 // the wide kernel leaves them by chunk, the thin one as said above.
-template <typename T16, int DH>
+template <typename T16, int DH, int PARTS>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_constant__ PrefixParams p, int share, int rows) {
   using M = Mma16<T16>;
   constexpr int E = DH / 32;  // elements a lane
@@ -477,22 +477,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
       lse += at;
       o += at * DH;
     };
-    // kJoinParts parts at a time: a lane finds one and its weight, then all add
+    // PARTS parts (of 4, 16) at a time: a lane finds one and its weight, then all add
     // them up.  What they need from before is found first, so that one wait for
     // memory is left once the partial results are there.
-    constexpr int kJoinParts = 16;
     float mx = -INFINITY, sum = 0.f, a[E] = {};
-    for (int c0 = 0; c0 * share + sub < n_all || c0 == 0; c0 += kJoinParts) {
-      const int c = (c0 + (lane & (kJoinParts - 1))) * share + sub;
-      const int count = min(kJoinParts, (n_all - sub + share - 1) / share - c0);
+    for (int c0 = 0; c0 * share + sub < n_all || c0 == 0; c0 += PARTS) {
+      const int c = (c0 + (lane & (PARTS - 1))) * share + sub;
+      const int count = min(PARTS, (n_all - sub + share - 1) / share - c0);
       const float *lse = nullptr, *mine = nullptr;
       if (c < n_all) place(c, lse, mine);
       const unsigned long long addr = reinterpret_cast<unsigned long long>(mine);
       if (c0 == 0 && i == 0 && held) pdl_wait();
-      const float z = c < n_all && lane < kJoinParts ? *lse : -INFINITY;
-      float v[kJoinParts][E];
+      const float z = c < n_all && lane < PARTS ? *lse : -INFINITY;
+      float v[PARTS][E];
 #pragma unroll
-      for (int k = 0; k < kJoinParts; ++k) {
+      for (int k = 0; k < PARTS; ++k) {
         const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, addr, k)) + lane * E;
         if (k >= count) {
 #pragma unroll
@@ -510,7 +509,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_prefix_join(const __grid_co
 #pragma unroll
       for (int e = 0; e < E; ++e) a[e] *= keep;
 #pragma unroll
-      for (int k = 0; k < kJoinParts; ++k) {
+      for (int k = 0; k < PARTS; ++k) {
         const float w = __shfl_sync(0xffffffffu, f, k);
 #pragma unroll
         for (int e = 0; e < E; ++e) a[e] += w * v[k][e];
@@ -742,8 +741,13 @@ cudaError_t launch_prefix(const PrefixParams& p, const PrefixPlan& plan, int ele
   const int share = plan.rows < 8ll * plan.sms ? kJoinWarps : 1;
   const int rows = static_cast<int>((plan.rows + 32ll * plan.sms - 1) / (32ll * plan.sms));
   const long long per = static_cast<long long>(kJoinWarps / share) * rows;
-  return launch_k(k_prefix_join<T16, DH>, dim3(static_cast<unsigned>((plan.rows + per - 1) / per)),
-                  dim3(kJoinWarps * 32), 0, s, dim3(1), true, p, share, rows);
+  const auto join = [&](auto kernel) {
+    return launch_k(kernel, dim3(static_cast<unsigned>((plan.rows + per - 1) / per)), dim3(kJoinWarps * 32), 0, s, dim3(1),
+                    true, p, share, rows);
+  };
+  // (few parts leave room for more warps an SM)
+  return plan.warps == 0 && plan.p_chunks + plan.s_chunks <= 4 ? join(k_prefix_join<T16, DH, 4>)
+                                                               : join(k_prefix_join<T16, DH, 16>);
 }
 
 }  // namespace

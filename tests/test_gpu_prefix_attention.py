@@ -350,6 +350,14 @@ def test_nan_stays_in_its_rows(T):
             assert torch.isfinite(out[1].float()).all()
 
 
+@pytest.mark.parametrize("B,Hkv,own,P", [(2, 2, 700, None), (8, 8, 700, None), (16, 8, 2000, None), (4, 8, 1500, 600),
+                                         (16, 8, 900, 900)])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_own_parts_in_chunks(B, Hkv, own, P, dh):
+    """Blocks whose own sequences are long enough to be split, joined afterwards."""
+    _run(B, 17, 4 * Hkv, Hkv, dh, "float16", [own - 37 * b for b in range(B)], [(B, P)] if P else [])
+
+
 @pytest.mark.parametrize("P", [0, 200])
 def test_more_than_32_bits_of_rows(P):
     """B T Hq head_dim past 2^31: the last entries of a batch whose other ones have no rows."""
