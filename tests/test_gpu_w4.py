@@ -138,6 +138,36 @@ def test_same_on_any_stream_and_when_recorded():
     assert torch.equal(ref, other) and torch.equal(ref, out)
 
 
+@pytest.mark.parametrize("M,K,group,fmt,zero", [(1, 2048, 32, "e2m1", False), (16, 12288, 64, "int4", True),
+                                                (24, 2048, 128, "int4", True)])
+def test_recordings_at_the_same_time(M, K, group, fmt, zero):
+    """Two recordings replayed together over new activations, beside eager calls: the bits of a call by itself."""
+    import torch
+    from block_diffusion_speculative_hidden_gb300 import gemm_w4
+    W, sc, X, z = _data(M, 700, K, group, fmt, zero, "bfloat16", "bfloat16")
+    runs = []
+    for _ in range(2):
+        r = dict(x=X.clone(), out=torch.zeros(M, 700, device="cuda"), graph=torch.cuda.CUDAGraph(),
+                 stream=torch.cuda.Stream())
+        gemm_w4(W, sc, r["x"], zero=z, group=group, fmt=fmt, out=r["out"])
+        torch.cuda.synchronize()
+        with torch.cuda.graph(r["graph"], stream=r["stream"]):
+            gemm_w4(W, sc, r["x"], zero=z, group=group, fmt=fmt, out=r["out"])
+        runs.append(r)
+    for step in range(3):
+        xs = [X * (step + 1), X.flip(0) * -1.5]
+        want = [gemm_w4(W, sc, x, zero=z, group=group, fmt=fmt) for x in xs]
+        for r, x in zip(runs, xs):
+            r["x"].copy_(x)
+        torch.cuda.synchronize()
+        for r in runs:
+            with torch.cuda.stream(r["stream"]):
+                r["graph"].replay()
+        beside = gemm_w4(W, sc, xs[0], zero=z, group=group, fmt=fmt)
+        torch.cuda.synchronize()
+        assert all(torch.equal(r["out"], w) for r, w in zip(runs, want)) and torch.equal(beside, want[0])
+
+
 @pytest.mark.parametrize("T,n", [(1, [1, 1, 1]), (17, [17, 3, 9])])
 def test_a_decode_step(T, n):
     """q, k, v of a few tokens from 4-bit weights, appended behind a shared prefix, attended to and projected:
