@@ -44,7 +44,12 @@ struct WideLayout {
   static constexpr int OFF_KV = Q_BYTES;
   static constexpr int OFF_RED = OFF_KV + NS * SLOT;        // [2][warp][lane] row maxima, sums
   static constexpr int OFF_BAR = OFF_RED + 2 * SOFT * 32 * 4;
-  static constexpr int SMEM = 1024 + OFF_BAR + 256;
+  // pack_item's result: a tile's tokens, a scan's sums, the group, the item.  (In
+  // bytes of their own: the warps read them until the end, and no barrier stands
+  // between a warp's last look and another's first row maximum.)
+  static constexpr int OFF_PACK = OFF_BAR + 256;
+  static constexpr int PACK_BYTES = kWideTile * 4 + 128 + 128 + 64;
+  static constexpr int SMEM = 1024 + OFF_PACK + PACK_BYTES;
   // TMEM: S, then O; with 128 dimensions P lies over S (each page's 16 keys in
   // the first 8 of its own 16 columns), with 64 there is room for it beside
   static constexpr bool P_APART = DH == 64;
@@ -248,9 +253,10 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
   pdl_trigger();  // (the kernels behind wait for this one's results on their own)
   const int rows_tile = wide_rows(p.G);
   Item it;
-  int* tokens = reinterpret_cast<int*>(red);  // (PACK; until the softmax begins its place is free)
+  int* tokens = reinterpret_cast<int*>(smem + L::OFF_PACK);  // (PACK)
   if constexpr (PACK) {
     Item* found = reinterpret_cast<Item*>(tokens + kWideTile + 64);
+    static_assert(L::THREADS / 32 <= 32 && sizeof(Item) <= 64 && alignof(Item) <= 16, "their places");
     if (!pack_item<L::THREADS / 32>(p, rows_tile / p.G, found, reinterpret_cast<int*>(smem + L::OFF_KV),
                                     tokens + kWideTile, tokens + kWideTile + 32, tokens))
       return pdl_wait();
