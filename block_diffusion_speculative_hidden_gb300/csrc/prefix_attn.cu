@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(ThinLayout<DH>::THREADS) k_prefix_thin(const _
   using L = ThinLayout<DH>;
   using M = Mma16<T16>;
   constexpr int KS = DH / 16, NR = kThinRows / 8;
+  constexpr float kLift = M::kLifted ? 15.f : 0.f;  // (m moves with every page: no weight is above 2^kLift)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   long long* first = reinterpret_cast<long long*>(smem + L::BYTES);
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(ThinLayout<DH>::THREADS) k_prefix_thin(const _
           float mx = fmaxf(z[h], z[2 + h]);
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          const float mn = fmaxf(m[j][h], mx), ms = mn == -INFINITY ? 0.f : mn;
+          const float mn = fmaxf(m[j][h], mx - kLift), ms = mn == -INFINITY ? 0.f : mn;
           al[h] = thin_ex2(m[j][h] - ms);
           m[j][h] = mn;
           z[h] = thin_ex2(z[h] - ms);

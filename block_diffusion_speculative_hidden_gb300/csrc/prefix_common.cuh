@@ -227,10 +227,19 @@ __device__ __forceinline__ Row find_row(const PrefixParams& p, const Item& it, i
   return w;
 }
 
+// Probabilities enter the second product in the cache's type, relative to
+// 2^(m - kLift), so that the largest is about 2^kLift.  Rounding them costs half
+// a step of the type each, as the one rounding of the output does (errors against
+// 64 bits 1.0 to 1.4 times those of fp32 probabilities); two products with a
+// high and a low half would cost as much again as the first.  fp16 steps no
+// finer than 2^-24: the lift moves that edge from 2^-24 of the largest weight to
+// 2^-24 - kLift, where even a million faint keys lose less than the output's half
+// step.  bf16 has the exponents to go without.
 template <typename T>
 struct Mma16;
 template <>
 struct Mma16<__nv_bfloat16> {
+  static constexpr bool kLifted = false;
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -245,6 +254,7 @@ struct Mma16<__nv_bfloat16> {
 };
 template <>
 struct Mma16<__half> {
+  static constexpr bool kLifted = true;
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "

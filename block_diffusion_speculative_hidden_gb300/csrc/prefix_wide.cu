@@ -7,7 +7,7 @@
 // query row (its TMEM lane), each with half of the keys and of the head's
 // dimensions.  While one CTA's softmax runs, the other's products do; with 64
 // dimensions S(j + 1) is made under the softmax of tile j as well.  m is the
-// maximum of a row's first tile and moves (O is then rescaled in TMEM) only
+// maximum of a row's first tile (less kLift) and moves (O is then rescaled in TMEM) only
 // when a later tile's P sums to 2^14 or more, so P stays within 16 bits and
 // most tiles need no maximum.
 //
@@ -235,6 +235,8 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p, int n_prefix) {
   using L = WideLayout<DH>;
   using M16 = Mma16<T16>;
+  // (64 keys of a half tile at 2^kLift sum to less than 2^kWideLazy)
+  constexpr float kLift = M16::kLifted ? 6.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(smem + L::OFF_RED);
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
       if (j == 0) {
         float top = row_top();
         top = fmaxf(top, partner(0, top));
-        m = top * p.scale_log2;
+        m = top * p.scale_log2 - kLift;
         l = make_p();
       } else {
         // P against the m so far.  Its sum shows whether m still serves: below
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
         } else {
           float top = row_top();
           top = fmaxf(top, partner(j & 1, top));
-          const float cand = fmaxf(m, top * p.scale_log2);
+          const float cand = fmaxf(m, top * p.scale_log2 - kLift);
           const float al = cand > m ? wide_ex2(m - cand) : 1.f;  // (m = -infinity: 0)
           m = cand;
           // (where P lies over S, S(j) was issued after P(j - 1) V was done)

@@ -479,7 +479,9 @@ dflash_status dflash_append_kv(const dflash_paged_kv* kv, const void* k, long lo
  * itself only if ld_q = n_q_heads * head_dim and it is the same address.
  * head_dim 64 or 128; n_q_heads a multiple of n_kv_heads.  Scores, running
  * maxima and sums and the output accumulate in fp32; probabilities enter the
- * second product in the cache's type.  What the cache holds past a length
+ * second product in the cache's type: each within half a step of its own, in
+ * fp16 also within 2^-31 of the largest weight (fainter keys count in the sum
+ * only, 2^10 of them below 2^-21 of the output).  What the cache holds past a length
  * has no effect (NaN included); a non-finite value within the tokens that
  * some row of an entry sees may reach all rows of that entry.
  *
