@@ -5,7 +5,7 @@
 // A row (batch entry b, token i) stands at slot seq_len - n + i of its
 // sequence; key and query elements x_i and x_{i+h} (h = head_dim / 2) rotate
 // as a pair by the table's angle of the row's position.
-#include "common.cuh"
+#include "decode_common.cuh"
 #include "kernels.cuh"
 
 namespace dflash {

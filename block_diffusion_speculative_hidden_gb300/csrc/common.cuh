@@ -23,9 +23,7 @@ enum : int {
   ST_WAIT_TIMEOUT = 4,     // a bounded device wait gave up
   ST_BAD_TOKEN = 8,        // a token id outside [0, vocab)
   ST_BAD_ROWS = 16,        // an n_rows entry outside [0, max_rows]
-  ST_BAD_BLOCK = 32,       // a block's sequence, prefix or group bounds out of range
-  ST_BAD_PAGE = 64,        // a page-table entry outside the pool
-  ST_BAD_POS = 128,        // a position outside the rotation table
+  ST_BAD_BLOCK = 32,       // a block's sequence, prefix or group bounds out of range (decode_common.cuh: further bits)
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait
@@ -258,23 +256,12 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
 }
 // 2-D tiled load of the box at (x = inner coordinate, y = row) into shared
 // memory; completion is signalled on `bar` as transaction bytes.
-__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
-  tma_load_2d_to(smem_u32(dst), map, bar, x, y);
-}
-// One thread of a converged warp, the same one every time.  Copies and MMAs
-// take their operands from uniform registers: where the whole warp computes
-// them alike and one thread is elected to issue, they are there already.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t is;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
-  return is != 0;
 }
 // Same, with an L2 eviction-priority hint (policy from createpolicy).
 __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,

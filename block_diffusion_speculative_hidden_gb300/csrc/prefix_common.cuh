@@ -7,7 +7,7 @@
 
 #include <type_traits>
 
-#include "common.cuh"
+#include "decode_common.cuh"
 #include "kernels.cuh"
 
 namespace dflash {

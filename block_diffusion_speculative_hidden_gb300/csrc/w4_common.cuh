@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "common.cuh"
+#include "decode_common.cuh"
 #include "internal.h"
 #include "tma_map.h"
 
