@@ -537,15 +537,17 @@ __global__ void __launch_bounds__(WideLayout<DH>::THREADS, 2)
       if (j == 0) {
         float top = row_top();
         top = fmaxf(top, partner(0, top));
-        m = top * p.scale_log2 - kLift;
+        // (rows without a query hold the caller's padding, or what was never
+        // written: against +infinity their P is 0 or NaN, and they never vote below)
+        m = at >= 0 ? top * p.scale_log2 - kLift : INFINITY;
         l = make_p();
       } else {
         // P against the m so far.  Its sum shows whether m still serves: below
         // 2^kWideLazy no term has grown past 16 bits.  Only where a row of the
-        // two warps fails that (an infinity or NaN included) the maxima are
-        // taken, m moves and P is made again.
+        // two warps fails that (an infinity included; a NaN stays one either way)
+        // the maxima are taken, m moves and P is made again.
         const float sum = make_p();
-        if (!wide_any(pair, !(sum < static_cast<float>(1 << kWideLazy)) || m == -INFINITY)) {
+        if (!wide_any(pair, sum >= static_cast<float>(1 << kWideLazy) || m == -INFINITY)) {
           l += sum;
         } else {
           float top = row_top();
