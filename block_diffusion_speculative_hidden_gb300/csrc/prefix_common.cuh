@@ -145,6 +145,12 @@ __device__ __forceinline__ void check_prefix(const PrefixParams& p, int row) {
   else if (p.seq_len[row] > p.max_pages * kPage) flag_status(p.status, ST_SEQ_TOO_LONG);
 }
 
+// Every group's prefix, of those without rows too (the whole CTA asks; a call, so
+// that what surrounds it keeps its registers).
+inline __device__ __noinline__ void check_groups(const PrefixParams& p) {
+  for (int g = threadIdx.x; g < p.NG; g += blockDim.x) check_prefix(p, p.prefix_seq[g]);
+}
+
 __device__ __forceinline__ void check_entry(const PrefixParams& p, int b, int row) {
   const int n = p.n_rows != nullptr ? p.n_rows[b] : p.T;
   if (n < 0 || n > p.T) flag_status(p.status, ST_BAD_ROWS);
@@ -178,13 +184,14 @@ __device__ __forceinline__ bool find_item(const PrefixParams& p, int index, int 
   const bool first = it.chunk == 0 && threadIdx.x == 0;  // the thread that reports
   if (it.shared) {
     Group g;
-    if (!bounds_ok(p) || !find_tile(p, tile, tile_rows, g)) return false;
+    if (!bounds_ok(p)) return false;
+    if (index == 0) check_groups(p);
+    if (!find_tile(p, tile, tile_rows, g)) return false;
     it.b0 = g.lo;
     it.row0 = g.tile * tile_rows;
     it.rows = (g.hi - g.lo) * p.T * p.G;
     it.tokens = g.tokens;
     it.table_row = g.row;
-    if (first) check_prefix(p, g.row);
   } else {
     const int b = tile / p.s_tiles;
     it.b0 = b;
