@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         for (int e = 0; e < 4; ++e)
           if (j * 8 + 2 * t4 + (e & 1) < p.M && row + (e >> 1) * 8 < p.N) {
             float* to = o + (e & 1 ? p.N : 0) + (e >> 1) * 8;
-            *to = acc[j][e] + (c > 0 ? *to : 0.f);
+            *to = acc[j][e] * (E2M1 ? 1.f : H::kSum) + (c > 0 ? *to : 0.f);
           }
     };
     bool open = false;  // a tile that this warp begins and others end
@@ -318,9 +318,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
                 for (int i = 0; i < 3; ++i) v[i] = look_up(word[h][w], i);
                 v[3] = H::e2m1x2(word[h][w] >> 24);
               } else {
-                // kMagic + the zero point, in both halves
-                const uint32_t bias = __byte_perm(z[h][g / 4], H::kMagic, 0x5050 | (g & 3) << 8 | (g & 3));
-                H::widen(word[h][w], bias, v);
+                H::widen(word[h][w], H::bias(z[h][g / 4], g & 3), v);
               }
               a[0][h] = v[0];
               a[0][2 + h] = v[1];

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(StreamLayout<GROUP, TILES, NB>::THREADS, 1)
               if constexpr (WPT == 4) *reinterpret_cast<uint4*>(word[h]) = *reinterpret_cast<const uint4*>(src);
               else if constexpr (WPT == 2) *reinterpret_cast<uint2*>(word[h]) = *reinterpret_cast<const uint2*>(src);
               else word[h][0] = *reinterpret_cast<const uint32_t*>(src);
-              bias[h] = E2M1 ? 0u : H::kMagic + (z[t][h] >> (8 * g) & 0xffu) * 0x00010001u;
+              bias[h] = E2M1 ? 0u : H::bias(z[t][h], g);
             }
             float d[NB][4];
 #pragma unroll
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(StreamLayout<GROUP, TILES, NB>::THREADS, 1)
       const float* src = sums + r / L::ROWS * (L::BYTES_O / 4) + m * L::PITCH_O + r % L::ROWS;
       float v = 0.f;
       for (int g = 0; g < kgroups; ++g) v += src[g * p.row_warps * (L::BYTES_O / 4)];
-      p.out[static_cast<long long>(m) * p.N + n] = v;
+      p.out[static_cast<long long>(m) * p.N + n] = v * (E2M1 ? 1.f : H::kSum);
     }
     __syncthreads();
   }

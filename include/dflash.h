@@ -516,8 +516,8 @@ typedef enum { DFLASH_W4_INT = 0, DFLASH_W4_E2M1 = 1 } dflash_w4_format;
  *
  * W: device uint8 [N][K / 2], byte j of a row holding the code of element 2j
  * in its low and of 2j + 1 in its high half.  DFLASH_W4_INT: w = code -
- * zero[n][k / group], with zero device uint8 [N][ceil(K / group)], each at
- * most 128, or NULL for 8.  DFLASH_W4_E2M1: a
+ * zero[n][k / group], with zero device uint8 [N][ceil(K / group)] (any value
+ * of a byte), or NULL for 8.  DFLASH_W4_E2M1: a
  * sign, two exponent bits of bias 1 and a mantissa bit (0, 0.5, 1, 1.5, 2, 3,
  * 4, 6 and their negatives); zero must be NULL.  scale: device
  * [N][ceil(K / group)] of type scale_elem; group 32, 64 or 128 (the last one
