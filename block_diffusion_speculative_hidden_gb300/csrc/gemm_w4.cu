@@ -23,6 +23,8 @@ extern "C" dflash_status dflash_gemm_w4(const void* W, int format, const void* s
   if (scale_elem != DFLASH_ELEM_F32 && scale_elem != DFLASH_ELEM_BF16 && scale_elem != DFLASH_ELEM_F16)
     return DFLASH_ERR_INVALID_ARG;
   if (M > 32 || K % 32 || (group != 32 && group != 64 && group != 128)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  // (row and unit counts, and the bytes of all activations, stay within 32 bits)
+  if (N > 1 << 30 || static_cast<long long>(M) * K > 1 << 29) return DFLASH_ERR_UNSUPPORTED_SHAPE;
   if (reinterpret_cast<uintptr_t>(W) % 16 || reinterpret_cast<uintptr_t>(X) % 16 ||
       reinterpret_cast<uintptr_t>(scale) % ss || reinterpret_cast<uintptr_t>(out) % 4)
     return DFLASH_ERR_INVALID_ARG;

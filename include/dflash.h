@@ -527,7 +527,8 @@ typedef enum { DFLASH_W4_INT = 0, DFLASH_W4_E2M1 = 1 } dflash_w4_format;
  * differences and scales apply to fp32 sums of a group, so nothing is rounded
  * below fp32.  status: device int32 (NULL: not reported), where a bounded
  * wait that gives up sets DFLASH_DEV_WAIT_TIMEOUT.  Asynchronous, allocates
- * nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE (M > 32, K, group), CUDA. */
+ * nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE (M > 32, K, group, N above
+ * 2^30 or M K above 2^29), CUDA. */
 dflash_status dflash_gemm_w4(const void* W, int format, const void* scale, int scale_elem, const void* zero, int N,
                              int K, int group, const void* X, int x_elem, int M, float* out, int* status,
                              dflash_stream stream);
