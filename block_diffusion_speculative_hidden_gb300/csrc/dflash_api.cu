@@ -505,7 +505,7 @@ dflash_status dflash_extend(dflash_ctx* ctx, const int32_t* n_rows, int first_se
                             dflash_stream stream) {
   if (ctx == nullptr || n_rows == nullptr) return DFLASH_ERR_INVALID_ARG;
   const dflash_config& g = ctx->cfg;
-  if (B < 1 || first_seq < 0 || first_seq + B > g.max_batch || max_rows < 1) return DFLASH_ERR_INVALID_ARG;
+  if (B < 1 || first_seq < 0 || B > g.max_batch - first_seq || max_rows < 1) return DFLASH_ERR_INVALID_ARG;
   if (max_rows > g.max_rows || static_cast<long long>(B) * max_rows > g.max_inject_rows)
     return DFLASH_ERR_UNSUPPORTED_SHAPE;
   ProfScope p(ctx, DFLASH_PROF_ROWWISE, 1, stream);
@@ -517,7 +517,7 @@ dflash_status dflash_inject_kv(dflash_ctx* ctx, const void* feats, const int32_t
                                int max_rows, dflash_stream stream) {
   if (ctx == nullptr || feats == nullptr || n_rows == nullptr) return DFLASH_ERR_INVALID_ARG;
   const dflash_config& g = ctx->cfg;
-  if (B < 1 || first_seq < 0 || first_seq + B > g.max_batch || max_rows < 1) return DFLASH_ERR_INVALID_ARG;
+  if (B < 1 || first_seq < 0 || B > g.max_batch - first_seq || max_rows < 1) return DFLASH_ERR_INVALID_ARG;
   if (max_rows > g.max_rows || static_cast<long long>(B) * max_rows > g.max_inject_rows)
     return DFLASH_ERR_UNSUPPORTED_SHAPE;
   if (reinterpret_cast<uintptr_t>(feats) % 16 != 0) return DFLASH_ERR_INVALID_ARG;
