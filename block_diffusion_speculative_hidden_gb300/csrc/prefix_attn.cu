@@ -785,7 +785,8 @@ dflash_status dflash_prefix_attention(const dflash_paged_kv* kv, const void* q, 
                                       void* workspace, size_t workspace_bytes, int* status, dflash_stream stream) {
   const dflash_status st = check_prefix(kv, n_q_heads, B, T, NG, max_prefix, max_len);
   if (st != DFLASH_OK) return st;
-  if (q == nullptr || out == nullptr || workspace == nullptr || !(scale >= 0.f) || scale > 3e38f)
+  // (times log2(e) it is an fp32 number still)
+  if (q == nullptr || out == nullptr || workspace == nullptr || !(scale >= 0.f) || scale > 2.35e38f)
     return DFLASH_ERR_INVALID_ARG;
   if (NG > 0 ? group_off == nullptr || prefix_seq == nullptr : group_off != nullptr || prefix_seq != nullptr)
     return DFLASH_ERR_INVALID_ARG;

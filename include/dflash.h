@@ -467,8 +467,8 @@ dflash_status dflash_append_kv(const dflash_paged_kv* kv, const void* k, long lo
  * sees tokens j <= L - n + i when causal is non-zero (the n rows are its last
  * n tokens) and all L otherwise.  out[b][i][h] = softmax(scale q k^T) v over
  * the tokens it sees, query head h reading kv head h / (n_q_heads /
- * n_kv_heads); scale 0 means 1 / sqrt(head_dim).  A row that sees nothing
- * gives 0, and its log-sum-exp is -infinity.  lse (device fp32
+ * n_kv_heads); scale is at most 2.35e38, and 0 means 1 / sqrt(head_dim).  A
+ * row that sees nothing gives 0, and its log-sum-exp is -infinity.  lse (device fp32
  * [B][T][n_q_heads]; NULL: none) gets log sum exp(scale q k^T).  Rows i >= n
  * of out and lse are left as they were.
  *
@@ -480,8 +480,7 @@ dflash_status dflash_append_kv(const dflash_paged_kv* kv, const void* k, long lo
  * head_dim 64 or 128; n_q_heads a multiple of n_kv_heads.  Scores, running
  * maxima and sums and the output accumulate in fp32; probabilities enter the
  * second product in the cache's type: each within half a step of its own, in
- * fp16 also within 2^-31 of the largest weight (fainter keys count in the sum
- * only, 2^10 of them below 2^-21 of the output).  What the cache holds past a length
+ * fp16 also within 2^-31 of the row's largest weight.  What the cache holds past a length
  * has no effect (NaN included); a non-finite value within the tokens that
  * some row of an entry sees may reach all rows of that entry.
  *
