@@ -135,6 +135,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
 //   - pdl_trigger() (which lets the successor start) comes after pdl_wait()
 //     in every CTA, so when a kernel starts, every kernel before its
 //     predecessor has completed.
+// The kernels of dflash_prefix_attention (prefix_attn.cu, prefix_wide.cu)
+// follow another pattern: they trigger first and wait in every CTA before it
+// leaves, so that a call's kernels run side by side.  A kernel that is
+// launched early behind them may start while all of that call is running.
+// What keeps it race-free: the call's first kernel is launched without the
+// attribute (all that came before has completed); a kernel's completion
+// implies its predecessor's, so that a successor's pdl_wait() covers the whole
+// call; and before that wait a successor touches nothing that any kernel of
+// the call writes (out, lse, the workspace, the status word), and writes
+// nothing that one reads (queries, lengths, tables, the pages).
 // pdl_wait() returns once the predecessor grid has completed and its memory
 // is visible; without a programmatic dependency both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -2,12 +2,12 @@
 // group scales,
 //     out[m][n] = sum_k X[m][k] scale[n][k/g] (code[n][k] - zero[n][k/g]).
 //
-// The differences code - zero (and the E2M1 values) are exact in bf16 and
-// fp16, so a block of 32 k enters the matrix instruction as it is, with fp32
-// sums, and the scale multiplies the block's fp32 sum.  The order of k inside
-// a block is free as long as weights and activations agree on it: thread t of
-// a quad holds codes 8t .. 8t+7 of the block (one 32-bit word), whose halves
-// come out of the word as pairs (k, k+4).
+// The differences code - zero (and the E2M1 values) are exact in bf16 (there in
+// 64ths) and fp16, so a block of 32 k enters the matrix instruction as it is,
+// with fp32 sums, and the scale multiplies the block's fp32 sum.  The order of
+// k inside a block is free as long as weights and activations agree on it:
+// thread t of a quad holds codes 8t .. 8t+7 of the block (one 32-bit word),
+// whose halves come out of the word as pairs (k, k+4).
 #include "w4_common.cuh"
 
 using namespace dflash;

@@ -47,14 +47,14 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
 // through `out`.  NB: blocks of 8 activation rows (the MMA's N).
 //
 // Bound by the instructions that widen codes: a warp takes some 400 for a unit
-// (16 x 256 codes: of 32 MMAs, 64 pairs of codes masked, subtracted and a third
-// of them shifted, 8 to 24 reads of activations, and its share of the ring),
+// (16 x 256 codes: of 32 MMAs, 64 pairs of codes masked, less their zero points,
+// a third of them shifted, 8 to 24 reads of activations, and its share of the ring),
 // four warps a scheduler issue 0.6 to 0.7 of them a cycle, and half to two
 // thirds of the integer pipe's and of shared memory's cycles are taken.  More
 // and smaller warps spill (20 warps: 41 us for the first of these).  Measured:
 // 24576 x 4096 in groups of 64 with zero points, 16 rows 22.2 us (2.5 TB/s of
 // codes, scales and zero points), one row 18.4; 6144 x 4096 in groups of 128,
-// one row 7.2; E2M1 codes, 151936 x 4096 in groups of 32, one row 80 us (4.4
+// one row 6.9; E2M1 codes, 151936 x 4096 in groups of 32, one row 80 us (4.4
 // TB/s).  Per-CTA k-groups that stream the activations as well (w4_stream.cu)
 // took 32.6, 26.1, 9.3 and 108.
 //

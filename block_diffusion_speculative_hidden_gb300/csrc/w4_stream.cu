@@ -62,7 +62,7 @@ struct StreamLayout {
 //
 // Bound by instructions as w4_resident.cuh is, and by what a tile's end costs
 // (24576 x 4096 in groups of 64: 24 rows 42 us, 32 rows 48; 2880 x 2880 in
-// groups of 32, 17 rows 9.7).
+// groups of 32, 17 rows 9.6).
 template <typename X, bool E2M1, int GROUP, int TILES, int NB>
 __global__ void __launch_bounds__(StreamLayout<GROUP, TILES, NB>::THREADS, 1)
     k_gemm_w4_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
