@@ -7,7 +7,7 @@
 // and the scale tiles, which tcgen05.cp puts into TMEM beside the accumulators
 // in front of the stage's four MMAs.  BN, the number of CTAs that share a
 // tile's k (a cluster; its partial sums meet in shared memory, added in the
-// order of the ranks) and the stages are chosen on the host (plan()).
+// order of the ranks) and the stages are chosen on the host (fp4_plan.h).
 //
 // Large products take pairs of CTAs (PAIR): two 128-row tiles of W beside each
 // other under one MMA of 256 rows, each CTA with half of X's rows in its shared memory.  One CTA alone is bound by
@@ -30,19 +30,14 @@
 #include <mutex>
 
 #include "fp4_common.cuh"
+#include "fp4_plan.h"
 #include "tma_map.h"
 
 namespace dflash {
 
 namespace {
 
-constexpr int kOutWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleCopyWarp = 11, kFp4Threads = 384;
-constexpr int kFp4Smem = 232448;
-constexpr int kRows = 128;              // rows of W a tile
-constexpr int kMaxBn = 256;             // the MMA's; scales from two tiles
-constexpr int kCodeRow = 128;           // bytes of 256 codes
-constexpr int kMaxStages = 8;
-constexpr int kMaxSplit = 8;
+constexpr int kCopyWarp = kOutWarps, kMmaWarp = 9, kScaleWarp = 10, kScaleCopyWarp = 11, kFp4Threads = 384;
 
 struct Fp4Params {
   const uint8_t *w_scales, *x_scales;
@@ -51,20 +46,21 @@ struct Fp4Params {
   long long tiles;                      // of all CTAs: n_tiles x m_tiles
   int M, N, kt, m_tiles, bn, stages;
   int last_mmas;                        // MMAs (64 k) of a row's last stage
-  int second, shared;                   // column of the second accumulator; blocks of 32 columns that it has of the first
+  int second;                           // column of the second accumulator
+  int shared_last, shared_first;        // blocks of 32 columns that they share: of the first one, of the second one
   int sc_first, tmem_cols;              // column of the scales; columns allocated
   int bulk;                             // out goes through shared memory: blocks of it that a warp has there (0: not)
   int* status;
 };
 
 // Shared memory: barriers, then (1024-aligned) the ring, then a block of out a warp.
-constexpr int kOutRows = 32;            // rows of out a block
 template <typename T>
 constexpr int kOutBlock = kOutRows * 32 * static_cast<int>(sizeof(T));
 struct Fp4Barriers {
   uint64_t full[kMaxStages], scaled[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   uint32_t tmem;
 };
+static_assert(sizeof(Fp4Barriers) <= kFp4Head, "the plan keeps room for them");
 
 // mbar_wait where no status word need be given.
 __device__ __forceinline__ bool fp4_wait(uint64_t* bar, uint32_t parity, int* status) {
@@ -382,7 +378,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       const uint32_t a = nth & 1, d = tmem + (a ? p.second : 0), x_off = CHUNKS * 4 + ((m0 & 127) >> 5);
       // an accumulator of its own is free once the tile before last is read out, one that shares columns with the
       // other once the last tile's part of these is (which comes after all of the tile before)
-      const uint32_t behind = p.shared > 0 ? 1 : 2;
+      const uint32_t behind = p.shared_first > 0 ? 1 : 2;
       if (nth >= behind) {
         uint64_t* const bar = &s.acc_empty[(nth - behind) & 1];
         const uint32_t parity_of = ((nth - behind) >> 1) & 1;
@@ -492,8 +488,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
       // Two of the warp's blocks at a time.  Columns that both accumulators have come first (the first one's last, the
       // second one's first), and the accumulator is given back as soon as these are in registers: behind their
       // stores the next tile's products waited 1.9 us a tile.
-      const bool down = a == 0 && p.shared > 0;
-      const int last = p.shared > 0 ? p.shared : blocks;
+      const bool down = a == 0 && p.shared_first > 0;
+      const int last = p.shared_first == 0 ? blocks : down ? p.shared_last : p.shared_first;
       bool gave = false;
       const auto give = [&]() {
         gave = true;
@@ -607,12 +603,6 @@ bool out_map(CUtensorMap* map, void* out, int elem, int M, int N, int size) {
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Fp4Plan {
-  int bn, m_tiles, split, stages, smem, second, shared, sc_first, cols, x_tiles, blocks;
-  unsigned grid;
-  bool pair;
-};
-
 // Clusters of n CTAs with an SM each that run at once: a GPC's SMs beyond whole clusters stay free.  Asked once a device.
 int clusters_at_once(int n, int sms) {
   static std::mutex mu;
@@ -639,65 +629,6 @@ int clusters_at_once(int n, int sms) {
     c = std::max(1, sms / n);
   }
   return c;
-}
-
-// Rows of X a tile, CTAs a tile, stages: the cheapest by a rough count of cycles.
-Fp4Plan plan(int format, int M, int N, int kt, int sms, int out_size) {
-  const int chunks = format == DFLASH_FP4_NV ? 4 : 2;
-  const long long n_tiles = (N + kRows - 1) / kRows;
-  Fp4Plan best{};
-  double best_cost = 0;
-  const auto consider = [&](int bn, int split, bool pair) {
-    const long long m_tiles = (M + bn - 1) / bn, tiles = (pair ? (n_tiles + 1) / 2 : n_tiles) * m_tiles;
-    if (split > 1 && tiles * split > 4ll * sms) return;
-    Fp4Plan c{};
-    c.bn = bn;
-    c.m_tiles = static_cast<int>(m_tiles);
-    c.split = split;
-    c.pair = pair;
-    // 128-row scale tiles that BN rows lie in, wherever they start
-    const int at = m_tiles > 1 ? 128 - std::min(128, bn & -bn) : 0;
-    c.x_tiles = (at + bn + 127) / 128;
-    if (pair && c.x_tiles != 2) return;
-    const int own = pair ? bn / 2 : bn;
-    const int stage = (kRows * kCodeRow + own * kCodeRow + chunks * 512 * (1 + c.x_tiles) + 1023) & ~1023;
-    // (a second block of out a warp, so that a copy is read while the next is written, where it costs no stage)
-    const int block = kOutWarps * kOutRows * 32 * out_size, room = kFp4Smem - 1024 - static_cast<int>(sizeof(Fp4Barriers));
-    c.stages = std::min(kMaxStages, (room - block) / stage);
-    c.blocks = std::min(kMaxStages, (room - 2 * block) / stage) == c.stages ? 2 : 1;
-    const int fixed = kFp4Smem - room + c.blocks * block;
-    // Two accumulators where a CTA has several tiles; where they do not fit beside the scales they share columns.
-    const int sets = c.stages * chunks * 4 * (1 + c.x_tiles);
-    const int team = pair ? 2 : split;
-    const long long at_once = team == 1 ? sms : clusters_at_once(team, sms), rounds = (tiles + at_once - 1) / at_once;
-    const bool one = split > 1 || tiles <= at_once;
-    c.sc_first = one ? bn : std::min(2 * bn, 512 - sets);
-    c.second = one ? 0 : c.sc_first - bn;
-    c.shared = one ? 0 : (2 * bn - c.sc_first + kOutRows - 1) / kOutRows;
-    c.cols = 32;
-    while (c.cols < c.sc_first + sets) c.cols *= 2;
-    if (c.sc_first < bn || c.cols > 512 || (split > 1 && bn * kRows * 4 > c.stages * stage)) return;
-    c.smem = fixed + c.stages * stage;
-    c.grid = static_cast<unsigned>((split > 1 ? tiles : std::min(tiles, at_once)) * team);
-    // (16 x 6144 x 4096: one CTA a tile 6.8 us, two 6.2, three, whose clusters do not run all at once, 10.6; 17 x 2560 x 9728: one
-    // 11.8, five 6.5)
-    // a stage: issuing it, shared memory's reads and writes, W's bytes from memory (once for all tiles beside each other)
-    const double per_k =
-        std::max({500., (4. * (4096 + 32 * own) + stage) / 128, 17408. / (23. * std::min<long long>(m_tiles, 8))});
-    double cost = 1500 + rounds * per_k * ((kt + split - 1) / split) + 300 + 8. * bn + (pair ? 1000 : 0);
-    cost += (rounds - 1) * (c.shared + 1) / 2 * 500.;
-    if (split > 1) cost += 1500 + (rounds - 1) * 2000 + 10. * bn;
-    if (best.bn == 0 || cost < best_cost) best = c, best_cost = cost;
-  };
-  for (int bn = 16; bn <= kMaxBn && bn < M + 16; bn += 16) {
-    // (a column of X's scales holds 32 rows, and the MMA takes them from an even column on)
-    if (bn < M && bn % 64) continue;
-    for (int split = 1; split <= kMaxSplit && split <= kt; ++split) consider(bn, split, false);
-  }
-  // (the lines of the scales are counted in 32 bits)
-  const bool lines = std::max<long long>(n_tiles + 2, M / kRows + 4) * kt * 8 < INT32_MAX;
-  for (int bn = 192; bn <= kMaxBn && lines && n_tiles > 1 && M > bn - 64; bn += 64) consider(bn, 1, true);
-  return best;
 }
 
 struct Fp4Maps {
@@ -750,7 +681,7 @@ extern "C" dflash_status dflash_gemm_fp4(const void* W, const void* w_scales, co
   if (e != cudaSuccess) return DFLASH_ERR_CUDA;
   Fp4Params p{};
   p.kt = (K + 255) / 256;
-  const Fp4Plan c = plan(format, M, N, p.kt, sms, size);
+  const Fp4Plan c = fp4_plan(format == DFLASH_FP4_NV, M, N, p.kt, sms, size, [&](int n) { return clusters_at_once(n, sms); });
   Fp4Maps maps{};
   const long long n_tiles = (N + kRows - 1) / kRows;
   if (!code_map(&maps.w, W, N, K, kRows) || !code_map(&maps.x, X, M, K, c.pair ? c.bn / 2 : c.bn)) return DFLASH_ERR_CUDA;
@@ -775,7 +706,8 @@ extern "C" dflash_status dflash_gemm_fp4(const void* W, const void* w_scales, co
   p.stages = c.stages;
   p.last_mmas = (K - (p.kt - 1) * 256 + 63) / 64;
   p.second = c.second;
-  p.shared = c.shared;
+  p.shared_last = c.shared_last;
+  p.shared_first = c.shared_first;
   p.sc_first = c.sc_first;
   p.tmem_cols = c.cols;
   p.status = status;
