@@ -47,7 +47,8 @@ __host__ __device__ __forceinline__ long long ws_ints(int n_pages, int n_seqs) {
   return kWsHead + 3ll * n_pages + 2ll * n_seqs;
 }
 
-__device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
+// (of any length from 0 on: a caller may cut to one next to 2^31)
+__device__ __forceinline__ int pages_of(int len) { return len / kPage + (len % kPage != 0); }
 
 constexpr int kStaged = 1024;  // entries whose sequences and lengths are kept in shared memory
 struct PlanShared {
