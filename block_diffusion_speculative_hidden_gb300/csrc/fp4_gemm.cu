@@ -200,6 +200,19 @@ __device__ __forceinline__ __nv_bfloat16 fp4_out<__nv_bfloat16>(float v) { retur
 template <>
 __device__ __forceinline__ __half fp4_out<__half>(float v) { return __float2half_rn(v); }
 
+// What sums are multiplied by: the product of the two tensors' scales, or, where that leaves fp32's normal range, both one
+// after the other, the larger one first (a sum is 0 or 2^-20 to 2^47: where it leaves the range in between, so does
+// the result).
+struct Fp4Alpha {
+  float a, b;
+  __device__ __forceinline__ float times(float v) const { return v * a * b; }
+};
+__device__ __forceinline__ Fp4Alpha fp4_alpha(const float* w, const float* x) {
+  const float f = w != nullptr ? *w : 1.f, g = x != nullptr ? *x : 1.f, h = f * g;
+  if (fabsf(h) >= 0x1p-126f && fabsf(h) < __int_as_float(0x7f800000)) return {h, 1.f};
+  return fabsf(f) >= fabsf(g) ? Fp4Alpha{f, g} : Fp4Alpha{g, f};
+}
+
 __device__ __forceinline__ void st_shared(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 __device__ __forceinline__ void st_shared(uint32_t a, __nv_bfloat16 v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(v)) : "memory");
@@ -417,11 +430,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     }
     __syncwarp();
   } else {
-    float alpha = 1.f;
-    if constexpr (NV) {
-      if (p.w_scale != nullptr) alpha = *p.w_scale;
-      if (p.x_scale != nullptr) alpha *= *p.x_scale;
-    }
+    Fp4Alpha alpha{1.f, 1.f};
+    if constexpr (NV) alpha = fp4_alpha(p.w_scale, p.x_scale);
     uint32_t n_tile = 0;
     bool ok = true;
     // two warps a quarter of the lanes, which take turns at the blocks of 32 columns
@@ -464,13 +474,13 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               st_shared(stage + ((to_row + i) * 32 + lane) * static_cast<int>(sizeof(T)),
-                        fp4_out<T>(NV ? __uint_as_float(x[i]) * alpha : __uint_as_float(x[i])));
+                        fp4_out<T>(alpha.times(__uint_as_float(x[i]))));
           } else if (nw + lane < p.N) {
             T* o = static_cast<T*>(p.out) + static_cast<long long>(m0 + c) * p.N + nw + lane;
             const int n = rows - c;
 #pragma unroll
             for (int i = 0; i < 16; ++i, o += p.N)
-              if (i < n) *o = fp4_out<T>(__uint_as_float(x[i]) * alpha);
+              if (i < n) *o = fp4_out<T>(alpha.times(__uint_as_float(x[i])));
           }
         };
         half(c, 0, v[0]);
@@ -521,11 +531,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     __syncwarp();
     cluster_sync_all();
     if (first < p.tiles) {
-      float alpha = 1.f;
-      if constexpr (NV) {
-        if (p.w_scale != nullptr) alpha = *p.w_scale;
-        if (p.x_scale != nullptr) alpha *= *p.x_scale;
-      }
+      Fp4Alpha alpha{1.f, 1.f};
+      if constexpr (NV) alpha = fp4_alpha(p.w_scale, p.x_scale);
       // (a warp a row, four of its columns a lane: with a column a thread and one row after the other 64 rows of two ranks took 4 us)
       const int n = static_cast<int>(first / p.m_tiles) * kRows + lane * 4, m0 = static_cast<int>(first % p.m_tiles) * p.bn;
       const int rows = min(p.bn, p.M - m0);
@@ -542,7 +549,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         T* const o = static_cast<T*>(p.out) + static_cast<long long>(m0 + r) * p.N + n;
         struct alignas(4 * sizeof(T)) Four {
           T t[4];
-        } four{{fp4_out<T>(sum.x * alpha), fp4_out<T>(sum.y * alpha), fp4_out<T>(sum.z * alpha), fp4_out<T>(sum.w * alpha)}};
+        } four{{fp4_out<T>(alpha.times(sum.x)), fp4_out<T>(alpha.times(sum.y)), fp4_out<T>(alpha.times(sum.z)),
+                   fp4_out<T>(alpha.times(sum.w))}};
         if (whole) {
           *reinterpret_cast<Four*>(o) = four;
         } else {

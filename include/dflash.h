@@ -580,7 +580,8 @@ dflash_status dflash_dequantize_fp4(const void* codes, const void* scales, int f
 /* Products of two such matrices of one format, beside dflash_gemm_w4 (whose
  * activations stay in 16 bits): out[m][n] = w_scale x_scale sum_k X[m][k] W[n][k],
  * any numbers of rows N of W and M of X up to 2^30.  Products are exact and
- * summed in fp32; the sum is rounded once to out_elem (out: device [M][N]).
+ * summed in fp32; the sum is multiplied in fp32 by the scales' product (by one after
+ * the other where that leaves fp32's normal range) and rounded to out_elem (out: device [M][N]).
  * status: device int32 (NULL: not reported), where a bounded wait that gives up
  * sets DFLASH_DEV_WAIT_TIMEOUT.  Asynchronous, allocates nothing.  Errors:
  * INVALID_ARG, UNSUPPORTED_SHAPE (as above), CUDA. */
