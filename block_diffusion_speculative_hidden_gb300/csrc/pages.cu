@@ -397,8 +397,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_plan_reserve(const PagesPar
   };
   // every entry's first place among the new pages, and among the copies (-1: none), before any count changes
   int32_t* place = to + p.n_pages;
-  int need = 0, copies = 0, full = 0;
-  for (int i0 = 0; i0 < p.B && !full; i0 += kPlanThreads) {
+  // (all are looked at, even behind those that want more than there is: what is wrong with an entry comes before
+  // pages that are missing for others)
+  int need = 0, copies = 0;
+  for (int i0 = 0; i0 < p.B; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
     int copy = 0, n = 0;
     if (i < p.B && !bad) bad |= want(i, n, copy);
@@ -409,13 +411,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_plan_reserve(const PagesPar
       place[2 * i] = need + static_cast<int>(upto & 0xffffffffffull);
       place[2 * i + 1] = copy ? copies + static_cast<int>(upto >> 40) : -1;
     }
-    need += static_cast<int>(all & 0xffffffffffull);
+    need = min(need + static_cast<int>(all & 0xffffffffffull), p.n_pages + 1);
     copies += static_cast<int>(all >> 40);
-    full = need > p.n_pages;
   }
-  // (what is wrong with an entry comes before pages that are missing for others)
   bad = cluster_or(s, bad, C, rank);
-  if (!bad && (full || !lowest_free(p, s, need, ids, C, rank))) bad = ST_POOL_EXHAUSTED;
+  if (!bad && (need > p.n_pages || !lowest_free(p, s, need, ids, C, rank))) bad = ST_POOL_EXHAUSTED;
   if (bad) {
     if (rank == 0 && threadIdx.x == 0) {
       p.ws[0] = 0;
