@@ -350,8 +350,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_dequantize_fp4(const DequantP
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t sc = two >> (8 * h) & 255u;
-      s[h] = (sc & 127u) == 127u ? __int_as_float(0x7fc00000) : e4m3_value(sc & 127u);
-      if (sc & 128u) s[h] = -s[h];
+      s[h] = sc < 127u ? e4m3_value(sc) : sc == 128u ? 0.f : __int_as_float(0x7fc00000);
     }
   } else {
     const uint32_t sc = *at;
@@ -388,9 +387,10 @@ __global__ void __launch_bounds__(kQuantThreads) k_dequantize_fp4(const DequantP
   }
 }
 
-// Row-major scales into tiles (a thread a 32-bit word of a row).
+// Row-major scales into tiles (a thread a 32-bit word of a row).  NV: the matrix unit's scales have no sign, so
+// bytes that have one become 127 (NaN), -0 becomes 0.
 __global__ void __launch_bounds__(kQuantThreads) k_fp4_tile_scales(const uint8_t* src, uint8_t* tiles, long long rows,
-                                                                   int n, int words) {
+                                                                   int n, int words, bool nv) {
   const long long u = static_cast<long long>(blockIdx.x) * kQuantThreads + threadIdx.x;
   const long long row = u / words;
   const int word = static_cast<int>(u - row * words);
@@ -398,7 +398,11 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_tile_scales(const uint8_t
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (row < rows && word * 4 + j < n) w |= static_cast<uint32_t>(src[row * n + word * 4 + j]) << (8 * j);
+    if (row < rows && word * 4 + j < n) {
+      uint32_t sc = src[row * n + word * 4 + j];
+      if (nv && sc > 127u) sc = sc == 128u ? 0u : 127u;
+      w |= sc << (8 * j);
+    }
   *reinterpret_cast<uint32_t*>(tiles + fp4_scale_at(row, word, words)) = w;
 }
 
@@ -435,7 +439,7 @@ dflash_status dflash_fp4_tile_scales(const void* scales, int format, long long r
   if (blocks == 0) return DFLASH_ERR_UNSUPPORTED_SHAPE;
   k_fp4_tile_scales<<<blocks, kQuantThreads, 0, stream>>>(static_cast<const uint8_t*>(scales),
                                                           static_cast<uint8_t*>(tiles), rows, K / fp4_group(format),
-                                                          words);
+                                                          words, format == DFLASH_FP4_NV);
   return cudaGetLastError() == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

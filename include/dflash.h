@@ -537,7 +537,8 @@ dflash_status dflash_gemm_w4(const void* W, int format, const void* scale, int s
  * and their negatives) under one step for a group of neighbours along k. */
 typedef enum {
   DFLASH_FP4_MX = 0, /* groups of 32, the step a power of two: the exponent + 127 in a byte (255: NaN) */
-  DFLASH_FP4_NV = 1  /* groups of 16, an E4M3 number (a byte; 127: NaN) times one fp32 number of the tensor */
+  DFLASH_FP4_NV = 1  /* groups of 16, an E4M3 number without a sign (a byte below 128; 127: NaN) times one fp32
+                        number of the tensor */
 } dflash_fp4_format;
 
 /* A matrix [rows][K] of either format, K a multiple of 32, is
@@ -554,7 +555,8 @@ typedef enum {
 size_t dflash_fp4_scales_size(int format, long long rows, int K);
 
 /* tiles (written in full, zeros where a row or group is missing) of row-major
- * scales, device uint8 [rows][K / group].  Asynchronous, allocates nothing. */
+ * scales, device uint8 [rows][K / group].  NV bytes with a sign become 127 (128, which
+ * is -0: 0).  Asynchronous, allocates nothing. */
 dflash_status dflash_fp4_tile_scales(const void* scales, int format, long long rows, int K, void* tiles,
                                      dflash_stream stream);
 
@@ -573,7 +575,8 @@ dflash_status dflash_quantize_fp4(const void* X, int x_elem, long long ld_x, lon
                                   const float* scale, void* codes, void* scales, dflash_stream stream);
 
 /* out (device [M][K], type out_elem, 16-byte aligned) = the values that codes and
- * scales stand for, in fp32 and rounded to the type.  Otherwise as above. */
+ * scales stand for, in fp32 and rounded to the type (NV bytes from 129 on: NaN; dflash_gemm_fp4
+ * does not tell them from others).  Otherwise as above. */
 dflash_status dflash_dequantize_fp4(const void* codes, const void* scales, int format, const float* scale, long long M,
                                     int K, void* out, int out_elem, dflash_stream stream);
 
