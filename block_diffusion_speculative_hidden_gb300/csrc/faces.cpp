@@ -131,6 +131,8 @@ int format_of(PyObject* o) {
   }
   throw Refusal{"fmt: mx or nv"};
 }
+// Columns are counted in 32 bits by the library's calls.
+void need_cols(int64_t cols) { need(cols <= INT32_MAX, "cols: too many columns"); }
 int64_t scale_bytes(int64_t rows, int64_t cols, int format) {
   return (rows + 127) / 128 * ((cols + 255) / 256) * (format == DFLASH_FP4_NV ? 2048 : 1024);
 }
@@ -178,6 +180,7 @@ PyObject* make_matrix(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(codes.dim() == 2 && codes.scalar_type() == at::kByte && codes.is_contiguous(), kCodes);
     const int64_t rows = codes.size(0), cols = 2 * codes.size(1);
     need(cols % 32 == 0, "cols: a multiple of 32");
+    need_cols(cols);
     const int dev = index_of(codes);
     constexpr const char* kScales = "scales: contiguous uint8 tiles of all rows, on the codes' device";
     const at::Tensor& scales = tensor(a[1], kScales);
@@ -274,6 +277,7 @@ PyObject* make_matrix_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int format = format_of(a[2]);
     const at::Tensor& like = tensor(a[4], "like: a tensor");
     need(rows > 0 && cols > 0 && cols % 32 == 0, "at least one row, cols a multiple of 32");
+    need_cols(cols);
     return reinterpret_cast<PyObject*>(matrix_room(rows, cols, format, scale_of(a[3], format, index_of(like)), like.device()));
   });
 }
@@ -290,7 +294,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t rows = x.size(0), cols = x.size(1);
     need(rows > 0 && cols > 0 && cols % 32 == 0, "x: at least one row, cols a multiple of 32");
     need(x.stride(1) == 1, "x: the entries of a row must be contiguous");
-    need(cols <= INT32_MAX, "x: too many columns");
+    need_cols(cols);
     const std::optional<at::Tensor> scale = scale_of(a[2], format, index_of(x));
     Matrix* m;
     if (a[3] == Py_None) {
