@@ -303,16 +303,17 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       constexpr const char* kOut = "out: the shape of x, fmt, its device";
       m = matrix(a[3], kOut);
       need(m->rows == rows && m->cols == cols && m->format == format && m->dev == index_of(x), kOut);
-      set_scale(m, scale);
       Py_INCREF(m);
     }
+    const float* const scale_at = scale ? static_cast<const float*>(scale->data_ptr()) : nullptr;
     const dflash_status code = dflash_quantize_fp4(
-        x.data_ptr(), elem, rows > 1 ? x.stride(0) : cols, rows, static_cast<int>(cols), format, m->scale_at,
+        x.data_ptr(), elem, rows > 1 ? x.stride(0) : cols, rows, static_cast<int>(cols), format, scale_at,
         const_cast<void*>(m->codes_at), const_cast<void*>(m->scales_at), on.stream);
     if (code != DFLASH_OK) {
       Py_DECREF(m);
       check(code, "dflash_quantize_fp4");
     }
+    set_scale(m, scale);  // (of the codes that m holds now)
     return reinterpret_cast<PyObject*>(m);
   });
 }

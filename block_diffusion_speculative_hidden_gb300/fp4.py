@@ -83,7 +83,7 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "mx", *, scale: Optional[torch.Tens
                  stream=None) -> Fp4:
     """x [rows, cols] (fp32, bf16 or fp16; rows may be apart) as microscaled
     4-bit floats; scale (nv): the tensor's number, e.g. its largest magnitude /
-    (448 * 6)."""
+    (448 * 6), which `out` then has in place of the one before."""
     if stream is not None:
         with _on(x.get_device(), stream):
             return quantize_fp4(x, fmt, scale=scale, out=out)
