@@ -21,6 +21,7 @@
 #include <new>
 #include <optional>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "dflash.h"
@@ -50,6 +51,23 @@ PyObject* faced(F&& f) {
   }
   END_HANDLE_TH_ERRORS
 }
+
+// f() while other Python threads run: outputs' memory and the launches, which may wait for room in the GPU's queue.
+// What f reads of Python's objects is read before.
+template <typename F>
+auto apart(F&& f) {
+  struct Released {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return f();
+}
+// A new reference until it is taken out.
+struct Hold {
+  PyObject* o;
+  ~Hold() { Py_XDECREF(o); }
+  PyObject* take() { return std::exchange(o, nullptr); }
+};
 
 // An error of the library, raised by the package's own check.
 void check(dflash_status code, const char* what) {
@@ -202,20 +220,20 @@ PyObject* make_matrix(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Room for a matrix, in one piece of memory.
-Matrix* matrix_room(int64_t rows, int64_t cols, int format, const std::optional<at::Tensor>& scale, at::Device device) {
-  const int64_t at = (rows * cols / 2 + 15) / 16 * 16;
-  const at::Tensor both = room({at + scale_bytes(rows, cols, format)}, at::kByte, device);
+// A matrix without memory, which take_room then gives it, in one piece.
+Matrix* shaped(int64_t rows, int64_t cols, int format, int dev) {
   Matrix* const m = new_matrix();
-  m->codes = both;
   m->rows = rows;
   m->cols = cols;
   m->format = format;
-  m->dev = index_of(both);
-  m->codes_at = both.data_ptr();
-  m->scales_at = static_cast<const uint8_t*>(both.data_ptr()) + at;
-  set_scale(m, scale);
+  m->dev = dev;
   return m;
+}
+void take_room(Matrix* m, at::Device device) {
+  const int64_t at = (m->rows * m->cols / 2 + 15) / 16 * 16;
+  m->codes = room({at + scale_bytes(m->rows, m->cols, m->format)}, at::kByte, device);
+  m->codes_at = m->codes.data_ptr();
+  m->scales_at = static_cast<const uint8_t*>(m->codes_at) + at;
 }
 // The views of one piece, when they are first asked for.
 void split(Matrix* m) {
@@ -278,7 +296,12 @@ PyObject* make_matrix_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& like = tensor(a[4], "like: a tensor");
     need(rows > 0 && cols > 0 && cols % 32 == 0, "at least one row, cols a multiple of 32");
     need_cols(cols);
-    return reinterpret_cast<PyObject*>(matrix_room(rows, cols, format, scale_of(a[3], format, index_of(like)), like.device()));
+    const std::optional<at::Tensor> scale = scale_of(a[3], format, index_of(like));
+    Matrix* const m = shaped(rows, cols, format, index_of(like));
+    Hold hold{reinterpret_cast<PyObject*>(m)};
+    apart([&] { take_room(m, like.device()); });
+    set_scale(m, scale);
+    return hold.take();
   });
 }
 
@@ -296,41 +319,54 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(x.stride(1) == 1, "x: the entries of a row must be contiguous");
     need_cols(cols);
     const std::optional<at::Tensor> scale = scale_of(a[2], format, index_of(x));
+    const bool fresh = a[3] == Py_None;
     Matrix* m;
-    if (a[3] == Py_None) {
-      m = matrix_room(rows, cols, format, scale, x.device());
+    if (fresh) {
+      m = shaped(rows, cols, format, index_of(x));
     } else {
       constexpr const char* kOut = "out: the shape of x, fmt, its device";
       m = matrix(a[3], kOut);
       need(m->rows == rows && m->cols == cols && m->format == format && m->dev == index_of(x), kOut);
       Py_INCREF(m);
     }
+    Hold hold{reinterpret_cast<PyObject*>(m)};
     const float* const scale_at = scale ? static_cast<const float*>(scale->data_ptr()) : nullptr;
-    const dflash_status code = dflash_quantize_fp4(
-        x.data_ptr(), elem, rows > 1 ? x.stride(0) : cols, rows, static_cast<int>(cols), format, scale_at,
-        const_cast<void*>(m->codes_at), const_cast<void*>(m->scales_at), on.stream);
-    if (code != DFLASH_OK) {
-      Py_DECREF(m);
-      check(code, "dflash_quantize_fp4");
-    }
+    const dflash_status code = apart([&] {
+      if (fresh) take_room(m, x.device());
+      return dflash_quantize_fp4(x.data_ptr(), elem, rows > 1 ? x.stride(0) : cols, rows, static_cast<int>(cols), format,
+                                 scale_at, const_cast<void*>(m->codes_at), const_cast<void*>(m->scales_at), on.stream);
+    });
+    check(code, "dflash_quantize_fp4");
     set_scale(m, scale);  // (of the codes that m holds now)
-    return reinterpret_cast<PyObject*>(m);
+    return hold.take();
   });
 }
 
-// out, or a new contiguous tensor [rows, cols] of dtype on the matrix's device
-at::Tensor rows_out(PyObject* out, PyObject* dtype, int64_t rows, int64_t cols, const Matrix* m, const char* what) {
-  if (out == Py_None) {
-    need(THPDtype_Check(dtype) && elem_of(reinterpret_cast<THPDtype*>(dtype)->scalar_type) >= 0,
-         "dtype: fp32, bf16 or fp16");
-    return room({rows, cols}, reinterpret_cast<THPDtype*>(dtype)->scalar_type, m->codes.device());
+// A contiguous output [rows, cols]: the caller's, or one to be taken on the matrix's device.
+struct RowsOut {
+  RowsOut(PyObject* out, PyObject* dtype, int64_t rows, int64_t cols, const Matrix* m, const char* what)
+      : rows(rows), cols(cols), device(m->codes.device()) {
+    if (out == Py_None) {
+      need(THPDtype_Check(dtype) && elem_of(reinterpret_cast<THPDtype*>(dtype)->scalar_type) >= 0,
+           "dtype: fp32, bf16 or fp16");
+      type = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
+      return;
+    }
+    t = tensor(out, what);
+    need(t.dim() == 2 && t.size(0) == rows && t.size(1) == cols && elem_of(t.scalar_type()) >= 0 && t.is_contiguous() &&
+             index_of(t) == m->dev,
+         what);
+    type = t.scalar_type();
   }
-  const at::Tensor& t = tensor(out, what);
-  need(t.dim() == 2 && t.size(0) == rows && t.size(1) == cols && elem_of(t.scalar_type()) >= 0 && t.is_contiguous() &&
-           index_of(t) == m->dev,
-       what);
-  return t;
-}
+  void* take() {
+    if (!t.defined()) t = room({rows, cols}, type, device);
+    return t.data_ptr();
+  }
+  int64_t rows, cols;
+  at::Device device;
+  at::ScalarType type;
+  at::Tensor t;
+};
 
 // dequantize(t, dtype, out)
 PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -338,12 +374,14 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     arguments(n, 3);
     const Matrix* m = matrix(a[0], "t: a matrix of 4-bit floats");
     const On on(m->dev);
-    const at::Tensor out =
-        rows_out(a[2], a[1], m->rows, m->cols, m, "out: contiguous fp32, bf16 or fp16 [rows, cols] on the codes' device");
-    check(dflash_dequantize_fp4(m->codes_at, m->scales_at, m->format, m->scale_at, m->rows, static_cast<int>(m->cols),
-                                out.data_ptr(), elem_of(out.scalar_type()), on.stream),
+    RowsOut out(a[2], a[1], m->rows, m->cols, m, "out: contiguous fp32, bf16 or fp16 [rows, cols] on the codes' device");
+    const float* const scale = m->scale_at;
+    check(apart([&] {
+            return dflash_dequantize_fp4(m->codes_at, m->scales_at, m->format, scale, m->rows, static_cast<int>(m->cols),
+                                         out.take(), elem_of(out.type), on.stream);
+          }),
           "dflash_dequantize_fp4");
-    return a[2] == Py_None ? wrap(out) : same(a[2]);
+    return a[2] == Py_None ? wrap(out.t) : same(a[2]);
   });
 }
 
@@ -355,13 +393,17 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const On on(w->dev);
     need(x->cols == w->cols && x->format == w->format && x->dev == w->dev, "X: the columns, format and device of W");
     need(x->rows <= INT32_MAX && w->rows <= INT32_MAX, "too many rows");
-    const at::Tensor out = rows_out(a[3], a[2], x->rows, w->rows, w,
-                                    "out: contiguous fp32, bf16 or fp16 [rows of X, rows of W] on the device of W");
-    check(dflash_gemm_fp4(w->codes_at, w->scales_at, w->scale_at, static_cast<int>(w->rows), x->codes_at, x->scales_at,
-                          x->scale_at, static_cast<int>(x->rows), static_cast<int>(w->cols), w->format, out.data_ptr(),
-                          elem_of(out.scalar_type()), ints(a[4], 1, w->dev, "status"), on.stream),
+    RowsOut out(a[3], a[2], x->rows, w->rows, w,
+                "out: contiguous fp32, bf16 or fp16 [rows of X, rows of W] on the device of W");
+    int* const status = ints(a[4], 1, w->dev, "status");
+    const float *const w_scale = w->scale_at, *const x_scale = x->scale_at;
+    check(apart([&] {
+            return dflash_gemm_fp4(w->codes_at, w->scales_at, w_scale, static_cast<int>(w->rows), x->codes_at, x->scales_at,
+                                   x_scale, static_cast<int>(x->rows), static_cast<int>(w->cols), w->format, out.take(),
+                                   elem_of(out.type), status, on.stream);
+          }),
           "dflash_gemm_fp4");
-    return a[3] == Py_None ? wrap(out) : same(a[3]);
+    return a[3] == Py_None ? wrap(out.t) : same(a[3]);
   });
 }
 
@@ -418,16 +460,19 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t *out_at = ints(a[6], B * (K + 1), dev, "out"), *n_at = ints(a[7], B, dev, "n_out");
     int32_t* status = ints(a[8], 1, dev, "status");
     at::Tensor out, count;
-    if (out_at == nullptr) {
-      out = room({B, K + 1}, at::kInt, target.device());
-      out_at = static_cast<int32_t*>(out.data_ptr());
-    }
-    if (n_at == nullptr) {
-      count = room({B}, at::kInt, target.device());
-      n_at = static_cast<int32_t*>(count.data_ptr());
-    }
-    check(dflash_verify_tokens(tokens, n_draft, target.data_ptr(), te, ld_t, draft, de, ld_d, ua, us, static_cast<int>(B),
-                               static_cast<int>(K), static_cast<int>(V), out_at, n_at, status, on.stream),
+    check(apart([&] {
+            if (out_at == nullptr) {
+              out = room({B, K + 1}, at::kInt, target.device());
+              out_at = static_cast<int32_t*>(out.data_ptr());
+            }
+            if (n_at == nullptr) {
+              count = room({B}, at::kInt, target.device());
+              n_at = static_cast<int32_t*>(count.data_ptr());
+            }
+            return dflash_verify_tokens(tokens, n_draft, target.data_ptr(), te, ld_t, draft, de, ld_d, ua, us,
+                                        static_cast<int>(B), static_cast<int>(K), static_cast<int>(V), out_at, n_at, status,
+                                        on.stream);
+          }),
           "dflash_verify_tokens");
     PyObject* r = PyTuple_New(2);
     if (r == nullptr) throw Raised{};
@@ -487,10 +532,7 @@ PyObject* make_pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto* p = reinterpret_cast<Pool*>(pool_type->tp_alloc(pool_type, 0));
     if (p == nullptr) throw Raised{};
     new (&p->layers) std::vector<void*>();
-    struct Hold {
-      PyObject* o;
-      ~Hold() { Py_XDECREF(o); }
-    } hold{reinterpret_cast<PyObject*>(p)};
+    Hold hold{reinterpret_cast<PyObject*>(p)};
     for (int i = 0; i < 5; ++i) {
       p->tensors[i] = i < 2 && !is_tensor(a[i]) ? PySequence_Tuple(a[i]) : same(a[i]);
       if (p->tensors[i] == nullptr) throw Raised{};
@@ -529,8 +571,7 @@ PyObject* make_pool(PyObject*, PyObject* const* a, Py_ssize_t n) {
     q.elem = static_cast<decltype(q.elem)>(elem);
     p->dev = dev;
     p->workspace = 4 * (64 + 3 * static_cast<size_t>(sizes[1]) + 2 * static_cast<size_t>(sizes[2]));
-    hold.o = nullptr;
-    return reinterpret_cast<PyObject*>(p);
+    return hold.take();
   });
 }
 
@@ -560,32 +601,38 @@ PyGetSetDef pool_members[] = {{"k", pool_tensor<0>, nullptr, nullptr, nullptr},
                               {"ref", pool_ref, nullptr, nullptr, nullptr},
                               {nullptr, nullptr, nullptr, nullptr, nullptr}};
 
-// The caller's workspace, or one that lives as long as this.
+// The caller's workspace, or one that is taken and lives as long as this.
 struct Space {
-  Space(const Pool* p, PyObject* o) {
-    if (o == Py_None) {
-      own = room({static_cast<int64_t>(p->workspace)}, at::kByte, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(p->dev)));
-      at = own.data_ptr();
-      bytes = p->workspace;
-      return;
-    }
+  Space(const Pool* p, PyObject* o) : dev(p->dev), bytes(p->workspace) {
+    if (o == Py_None) return;
     constexpr const char* kWhat = "workspace: contiguous, the pool's device";
     const at::Tensor& t = tensor(o, kWhat);
     need(index_of(t) == p->dev && t.is_contiguous(), kWhat);
     at = t.data_ptr();
     bytes = t.nbytes();
+    given = true;
   }
-  at::Tensor own;
-  void* at;
+  void* take() {
+    if (!given) {
+      own = room({static_cast<int64_t>(bytes)}, at::kByte, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+      at = own.data_ptr();
+    }
+    return at;
+  }
+  int dev;
   size_t bytes;
+  bool given = false;
+  at::Tensor own;
+  void* at = nullptr;
 };
 int count_of(int64_t n) {
   need(n <= INT32_MAX, "too many entries");
   return static_cast<int>(n);
 }
 int64_t entries(PyObject* o, const char* what) { return tensor(o, what).numel(); }
-PyObject* done(dflash_status code, const char* what) {
-  check(code, what);
+template <typename F>
+PyObject* done(const char* what, F&& f) {
+  check(apart(f), what);
   Py_RETURN_NONE;
 }
 
@@ -598,8 +645,10 @@ PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t B = entries(a[1], "src: contiguous int32");
     const int32_t *src = ints(a[1], B, p->dev, "src"), *dst = ints(a[2], B, p->dev, "dst");
     int* status = ints(a[4], 1, p->dev, "status");
-    const Space ws(p, a[3]);
-    return done(dflash_pages_fork(&p->pool, src, dst, count_of(B), ws.at, ws.bytes, status, on.stream), "dflash_pages_fork");
+    Space ws(p, a[3]);
+    return done("dflash_pages_fork", [&] {
+      return dflash_pages_fork(&p->pool, src, dst, count_of(B), ws.take(), ws.bytes, status, on.stream);
+    });
   });
 }
 
@@ -613,8 +662,9 @@ PyObject* truncate_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       : a[1] != Py_None ? entries(a[1], "new_len: contiguous int32")
                                         : p->pool.n_seqs;
     const int32_t *seq = ints(a[2], B, p->dev, "seq"), *len = ints(a[1], B, p->dev, "new_len");
-    return done(dflash_pages_truncate(&p->pool, seq, len, count_of(B), ints(a[3], 1, p->dev, "status"), on.stream),
-                "dflash_pages_truncate");
+    int* status = ints(a[3], 1, p->dev, "status");
+    return done("dflash_pages_truncate",
+                [&] { return dflash_pages_truncate(&p->pool, seq, len, count_of(B), status, on.stream); });
   });
 }
 
@@ -627,9 +677,10 @@ PyObject* reserve_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t B = entries(a[1], "n_rows: contiguous int32");
     const int32_t *seq = ints(a[2], B, p->dev, "seq"), *rows = ints(a[1], B, p->dev, "n_rows");
     int* status = ints(a[4], 1, p->dev, "status");
-    const Space ws(p, a[3]);
-    return done(dflash_pages_reserve(&p->pool, seq, rows, count_of(B), ws.at, ws.bytes, status, on.stream),
-                "dflash_pages_reserve");
+    Space ws(p, a[3]);
+    return done("dflash_pages_reserve", [&] {
+      return dflash_pages_reserve(&p->pool, seq, rows, count_of(B), ws.take(), ws.bytes, status, on.stream);
+    });
   });
 }
 
@@ -644,8 +695,9 @@ PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
             *refs = ints(a[2], q.n_pages, p->dev, "refs_out"), *map = ints(a[3], q.n_pages, p->dev, "page_map"),
             *used = ints(a[4], 1, p->dev, "n_used");
     int* status = ints(a[6], 1, p->dev, "status");
-    const Space ws(p, a[5]);
-    return done(dflash_pages_compact(&q, table, refs, map, used, ws.at, ws.bytes, status, on.stream), "dflash_pages_compact");
+    Space ws(p, a[5]);
+    return done("dflash_pages_compact",
+                [&] { return dflash_pages_compact(&q, table, refs, map, used, ws.take(), ws.bytes, status, on.stream); });
   });
 }
 
@@ -658,8 +710,9 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(from->dev == to->dev, "both pools on one device");
     const int64_t B = entries(a[1], "src: contiguous int32");
     const int32_t *dst = ints(a[2], B, to->dev, "dst"), *src = ints(a[1], B, to->dev, "src");
-    return done(dflash_pages_copy(&to->pool, &from->pool, dst, src, count_of(B), ints(a[4], 1, to->dev, "status"), on.stream),
-                "dflash_pages_copy");
+    int* status = ints(a[4], 1, to->dev, "status");
+    return done("dflash_pages_copy",
+                [&] { return dflash_pages_copy(&to->pool, &from->pool, dst, src, count_of(B), status, on.stream); });
   });
 }
 
