@@ -69,9 +69,17 @@ def _torch_dir() -> str:
 def _compile_faces() -> str:
     src, obj = os.path.join(CSRC, "faces.cpp"), os.path.join(BUILD, "faces.o")
     include = os.path.join(os.path.dirname(PKG), "include")
-    # (the object is of one PyTorch: an older one's headers or libraries are another reason to compile)
-    deps = [src, os.path.join(include, "dflash.h"), os.path.join(_torch_dir(), "version.py")]
-    if os.path.exists(obj) and all(os.path.getmtime(obj) >= os.path.getmtime(d) for d in deps):
+    # The object is of one PyTorch and one Python, whose files may be older than it: what it was compiled
+    # for stands beside it.
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        want = "\n".join([_torch_dir(), f.read(), sys.version, sysconfig.get_paths()["include"]])
+    stamp = obj + ".for"
+    have = None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            have = f.read()
+    deps = [src, os.path.join(include, "dflash.h")]
+    if os.path.exists(obj) and have == want and all(os.path.getmtime(obj) >= os.path.getmtime(d) for d in deps):
         return obj
     inc = os.path.join(_torch_dir(), "include")
     cmd = [_cxx(), "-std=c++17", "-O2", "-fPIC", "-Wall",
@@ -82,6 +90,8 @@ def _compile_faces() -> str:
     r = subprocess.run([*cmd, "-I", include, "-c", src, "-o", obj], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiling {src} failed:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(want)
     return obj
 
 
