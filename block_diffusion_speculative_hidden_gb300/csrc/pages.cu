@@ -15,6 +15,7 @@
 // barriers take longer, 9.8 and 27, of 256 11.8 and 31; 16 CTAs 8.8 and 23.6, but a small compaction 11.4 against 10.8), copying by memory
 // (2900 of 7001 pages of 5 layers, 1.05 GB read and written, 166 us with the plan: 6.3 TB/s).
 #include <algorithm>
+#include <initializer_list>
 
 #include "decode_common.cuh"
 #include "internal.h"
@@ -705,6 +706,38 @@ cudaError_t launch_copy(const dflash_page_pool& to, const dflash_page_pool& from
 
 dflash_status answer(cudaError_t e) { return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA; }
 
+// n entries (or bytes) of a caller's array, null for none.
+struct Span {
+  const void* at;
+  long long bytes;
+};
+Span ints(const int32_t* a, long long n) { return {a, 4 * n}; }
+bool apart(const Span& a, const Span& b) {
+  const auto lo = [](const Span& s) { return reinterpret_cast<uintptr_t>(s.at); };
+  return a.at == nullptr || b.at == nullptr || lo(a) + a.bytes <= lo(b) || lo(b) + b.bytes <= lo(a);
+}
+
+// Whether a call's arrays lie apart from the pool's and from its workspace.  (Entries are read, checked and read again
+// while tables, lengths, counts and lists are written.)
+bool apart(const dflash_page_pool& q, const PagesParams& p, std::initializer_list<Span> arrays) {
+  const Span own[] = {ints(q.page_table, static_cast<long long>(q.n_seqs) * q.max_pages), ints(q.seq_len, q.n_seqs),
+                      ints(q.refs, q.n_pages)},
+             ws = {p.ws, p.ws != nullptr ? 4 * ws_ints(q.n_pages, q.n_seqs) : 0};
+  for (const Span& o : own) {
+    if (!apart(ws, o)) return false;
+    for (const Span& a : arrays)
+      if (!apart(a, o)) return false;
+  }
+  for (const Span& a : arrays)
+    if (!apart(a, ws)) return false;
+  return true;
+}
+
+// (The lengths themselves, of entry i for sequence i: its thread reads them before it writes them.)
+const int32_t* by_itself(const dflash_page_pool& q, const int32_t* seq, const int32_t* b) {
+  return seq == nullptr && b == q.seq_len ? nullptr : b;
+}
+
 // Counts and workspace of a call on B sequences.
 dflash_status call_ok(const dflash_page_pool* q, int B, const void* ws, size_t bytes, const int* status) {
   const dflash_status e = pool_ok(q);
@@ -732,6 +765,7 @@ dflash_status dflash_pages_fork(const dflash_page_pool* pool, const int32_t* src
   if (c != DFLASH_OK) return c;
   if (src == nullptr || dst == nullptr || off(src, 4) || off(dst, 4)) return DFLASH_ERR_INVALID_ARG;
   const PagesParams p = params(*pool, src, dst, B, workspace, status);
+  if (!apart(*pool, p, {ints(src, B), ints(dst, B), ints(status, 1)})) return DFLASH_ERR_INVALID_ARG;
   static FuncAttr attr;
   cudaError_t e = launch_plan(k_plan_fork, attr, p, 2ll * B * pool->max_pages + pool->n_pages, 2, stream);
   if (e != cudaSuccess) return DFLASH_ERR_CUDA;
@@ -748,6 +782,7 @@ dflash_status dflash_pages_truncate(const dflash_page_pool* pool, const int32_t*
   if (c != DFLASH_OK) return c;
   if (B < 1 || B > pool->n_seqs || off(seq, 4) || off(new_len, 4) || off(status, 4)) return DFLASH_ERR_INVALID_ARG;
   const PagesParams p = params(*pool, seq, new_len, B, nullptr, status);
+  if (!apart(*pool, p, {ints(seq, B), ints(by_itself(*pool, seq, new_len), B), ints(status, 1)})) return DFLASH_ERR_INVALID_ARG;
   static FuncAttr attr;
   return answer(launch_plan(k_plan_truncate, attr, p, static_cast<long long>(B) * pool->max_pages, 1, stream));
 }
@@ -758,6 +793,7 @@ dflash_status dflash_pages_reserve(const dflash_page_pool* pool, const int32_t* 
   if (c != DFLASH_OK) return c;
   if (n_rows == nullptr || off(seq, 4) || off(n_rows, 4)) return DFLASH_ERR_INVALID_ARG;
   const PagesParams p = params(*pool, seq, n_rows, B, workspace, status);
+  if (!apart(*pool, p, {ints(seq, B), ints(by_itself(*pool, seq, n_rows), B), ints(status, 1)})) return DFLASH_ERR_INVALID_ARG;
   static FuncAttr attr;
   cudaError_t e = launch_plan(k_plan_reserve, attr, p, pool->n_pages, 1, stream);
   if (e != cudaSuccess) return DFLASH_ERR_CUDA;
@@ -775,12 +811,18 @@ dflash_status dflash_pages_compact(const dflash_page_pool* pool, int32_t* table_
   if (c != DFLASH_OK) return c;
   if (off(table_out, 4) || off(refs_out, 4) || off(page_map, 4) || off(n_used, 4)) return DFLASH_ERR_INVALID_ARG;
   PagesParams p = params(*pool, nullptr, nullptr, 0, workspace, status);
+  const long long entries = static_cast<long long>(pool->n_seqs) * pool->max_pages;
+  // (the pool's own arrays may be named as outputs)
+  if (table_out == pool->page_table) table_out = nullptr;
+  if (refs_out == pool->refs) refs_out = nullptr;
+  if (!apart(*pool, p, {ints(table_out, entries), ints(refs_out, pool->n_pages), ints(page_map, pool->n_pages), ints(n_used, 1),
+                        ints(status, 1)}))
+    return DFLASH_ERR_INVALID_ARG;
   p.table_out = table_out != nullptr ? table_out : pool->page_table;
   p.refs_out = refs_out != nullptr ? refs_out : pool->refs;
   p.page_map = page_map;
   p.n_used = n_used;
   static FuncAttr attr;
-  const long long entries = static_cast<long long>(pool->n_seqs) * pool->max_pages;
   cudaError_t e = launch_plan(k_plan_compact, attr, p, pool->n_pages + entries, 0, stream);
   if (e != cudaSuccess) return DFLASH_ERR_CUDA;
   // (at least as many threads as the table has entries, up to a full GPU)

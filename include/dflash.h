@@ -652,8 +652,9 @@ typedef struct {
  * NULL: not reported) and changes nothing.  New pages are the free ones of the
  * lowest ids, in the order of the entries.  workspace: device, 16-byte aligned, at least
  * dflash_pages_workspace bytes; it carries nothing from call to call, and calls
- * that may run at the same time need one each (and pools of their own).
- * Asynchronous, allocate nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE (head_dim, more
+ * that may run at the same time need one each (and pools of their own).  A call's arrays
+ * lie apart from the pool's and from the workspace (INVALID_ARG), but for the lengths
+ * themselves as numbers of a call without seq.  Asynchronous, allocate nothing.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE (head_dim, more
  * than 128 layers, 2^20 pages, 2^19 sequences), WORKSPACE, CUDA. */
 size_t dflash_pages_workspace(const dflash_page_pool* pool);
 
