@@ -32,6 +32,17 @@ __device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
+// The bytes of a caller's array, null for none; whether two of them share none.
+struct Span {
+  const void* at;
+  long long bytes;
+};
+inline Span ints(const int32_t* a, long long n) { return {a, 4 * n}; }
+inline bool apart(const Span& a, const Span& b) {
+  const auto lo = [](const Span& s) { return reinterpret_cast<uintptr_t>(s.at); };
+  return a.at == nullptr || b.at == nullptr || lo(a) + a.bytes <= lo(b) || lo(b) + b.bytes <= lo(a);
+}
+
 // A kernel that may start before its predecessor completes (it waits first), in clusters of `cluster` blocks; as launch_k, but
 // the driver picks the L1 cache's share: with all of it given to shared memory, streams through L1 are slower (quantising
 // 8192 rows of 12,288 42.8 us against 53.6, taking back 38.7 against 47.9).

@@ -706,17 +706,6 @@ cudaError_t launch_copy(const dflash_page_pool& to, const dflash_page_pool& from
 
 dflash_status answer(cudaError_t e) { return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA; }
 
-// n entries (or bytes) of a caller's array, null for none.
-struct Span {
-  const void* at;
-  long long bytes;
-};
-Span ints(const int32_t* a, long long n) { return {a, 4 * n}; }
-bool apart(const Span& a, const Span& b) {
-  const auto lo = [](const Span& s) { return reinterpret_cast<uintptr_t>(s.at); };
-  return a.at == nullptr || b.at == nullptr || lo(a) + a.bytes <= lo(b) || lo(b) + b.bytes <= lo(a);
-}
-
 // Whether a call's arrays lie apart from the pool's and from its workspace.  (Entries are read, checked and read again
 // while tables, lengths, counts and lists are written.)
 bool apart(const dflash_page_pool& q, const PagesParams& p, std::initializer_list<Span> arrays) {

@@ -389,6 +389,14 @@ extern "C" dflash_status dflash_verify_tokens(const int32_t* tokens, const int32
   // (the last row's offset in bytes stays inside 63 bits)
   const long long rows = static_cast<long long>(B) * (K + 1ll);
   if (ld_t > INT64_MAX / 8 / rows || (draft != nullptr && ld_d > INT64_MAX / 8 / rows)) return DFLASH_ERR_UNSUPPORTED_SHAPE;
+  // (a cluster's CTAs judge the drafts each by itself, while one of them may already write)
+  const Span in[] = {ints(tokens, static_cast<long long>(B) * K), ints(n_draft, B), {u_accept, 4ll * B * K}, {u_sample, 4ll * B},
+                     {target, ((rows - 1) * ld_t + V) * ts}, {draft, ((rows - B - 1) * ld_d + V) * ds}},
+             outs[] = {ints(out, rows), ints(n_out, B), ints(status, 1)};
+  for (const Span& o : outs)
+    for (const Span& i : in)
+      if (!apart(o, i)) return DFLASH_ERR_INVALID_ARG;
+  if (!apart(outs[0], outs[1]) || !apart(outs[0], outs[2]) || !apart(outs[1], outs[2])) return DFLASH_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

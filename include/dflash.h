@@ -613,7 +613,8 @@ dflash_status dflash_gemm_fp4(const void* W, const void* w_scales, const float* 
  * the total.  Differences are exact; sums of 512 entries are within 2^-27 (as a rule
  * 2^-36) of the largest among them and are added in double, in a fixed order.
  * out[b] (device int32 [B][K + 1]) gets the r tokens, the drawn one and -1
- * behind it, n_out[b] (device int32 [B]) r + 1; they must not overlap the inputs.
+ * behind it, n_out[b] (device int32 [B]) r + 1; they must not overlap the inputs or
+ * each other (INVALID_ARG).
  *
  * On the device an entry with n out of range (BAD_ROWS), a token outside
  * [0, V) (BAD_TOKEN), or a weight, total or random number that cannot be one
