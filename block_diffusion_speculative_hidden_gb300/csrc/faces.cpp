@@ -299,7 +299,8 @@ PyObject* make_matrix_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const std::optional<at::Tensor> scale = scale_of(a[3], format, index_of(like));
     Matrix* const m = shaped(rows, cols, format, index_of(like));
     Hold hold{reinterpret_cast<PyObject*>(m)};
-    apart([&] { take_room(m, like.device()); });
+    const at::Device device = like.device();
+    apart([&] { take_room(m, device); });
     set_scale(m, scale);
     return hold.take();
   });
@@ -331,12 +332,15 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     Hold hold{reinterpret_cast<PyObject*>(m)};
     const float* const scale_at = scale ? static_cast<const float*>(scale->data_ptr()) : nullptr;
-    const dflash_status code = apart([&] {
-      if (fresh) take_room(m, x.device());
-      return dflash_quantize_fp4(x.data_ptr(), elem, rows > 1 ? x.stride(0) : cols, rows, static_cast<int>(cols), format,
-                                 scale_at, const_cast<void*>(m->codes_at), const_cast<void*>(m->scales_at), on.stream);
-    });
-    check(code, "dflash_quantize_fp4");
+    const void* const x_at = x.data_ptr();
+    const int64_t ld = rows > 1 ? x.stride(0) : cols;
+    const at::Device device = x.device();
+    check(apart([&] {
+            if (fresh) take_room(m, device);
+            return dflash_quantize_fp4(x_at, elem, ld, rows, static_cast<int>(cols), format, scale_at,
+                                       const_cast<void*>(m->codes_at), const_cast<void*>(m->scales_at), on.stream);
+          }),
+          "dflash_quantize_fp4");
     set_scale(m, scale);  // (of the codes that m holds now)
     return hold.take();
   });
@@ -459,17 +463,19 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* n_draft = ints(a[5], B, dev, "n_draft");
     int32_t *out_at = ints(a[6], B * (K + 1), dev, "out"), *n_at = ints(a[7], B, dev, "n_out");
     int32_t* status = ints(a[8], 1, dev, "status");
+    const void* const target_at = target.data_ptr();
+    const at::Device device = target.device();
     at::Tensor out, count;
     check(apart([&] {
             if (out_at == nullptr) {
-              out = room({B, K + 1}, at::kInt, target.device());
+              out = room({B, K + 1}, at::kInt, device);
               out_at = static_cast<int32_t*>(out.data_ptr());
             }
             if (n_at == nullptr) {
-              count = room({B}, at::kInt, target.device());
+              count = room({B}, at::kInt, device);
               n_at = static_cast<int32_t*>(count.data_ptr());
             }
-            return dflash_verify_tokens(tokens, n_draft, target.data_ptr(), te, ld_t, draft, de, ld_d, ua, us,
+            return dflash_verify_tokens(tokens, n_draft, target_at, te, ld_t, draft, de, ld_d, ua, us,
                                         static_cast<int>(B), static_cast<int>(K), static_cast<int>(V), out_at, n_at, status,
                                         on.stream);
           }),
