@@ -570,7 +570,7 @@ dflash_status dflash_fp4_tile_scales(const void* scales, int format, long long r
  * that holds an infinity or NaN gets the step NaN.  The scales of rows 0 .. M-1
  * are written, the groups behind K as zeros.  Asynchronous, allocates nothing.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (K no multiple of 32 or above 2^24,
- * M above 2^30, 2^35 elements and more), CUDA. */
+ * M above 2^30, 2^35 elements and more with K in whole 256s), CUDA. */
 dflash_status dflash_quantize_fp4(const void* X, int x_elem, long long ld_x, long long M, int K, int format,
                                   const float* scale, void* codes, void* scales, dflash_stream stream);
 
